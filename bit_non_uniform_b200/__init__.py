@@ -11,6 +11,9 @@ The calls mirror ``include/cq.h``:
 * ``cq_decode(packed, scales, ab, K, B, G)``    -> W [N][K] (float32 / bfloat16)
 * ``cq_gemm(x, packed, scales, ab, N, K, B, G)`` -> y [M][N] (or [M][N/2])
 * ``cq_moe_grouped_gemm(tokens, topk_ids, ...)`` -> per-route / combined outputs
+* ``cq_linear_i8(x, wq, wscale)`` / ``cq_gemm_i8(xq, absmax, wq, wscale)`` -> y, INT8 weights
+* ``cq_moe_i8(tokens, topk_ids, topk_w, w_gu, s_gu, w_dn, s_dn)`` -> the layer on INT8 experts
+* ``cq_moe_route(logits, k)``                   -> (topk_ids, topk_w)
 """
 from __future__ import annotations
 
@@ -26,6 +29,7 @@ LIB_PATH = os.path.join(HERE, "libcq.so")
 MIDRISE, MIDTREAD = 0, 1
 F32, BF16 = 0, 1
 EPI_NONE, EPI_SWIGLU = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 _STATUS = {
     0: "ok", 1: "invalid argument", 2: "unsupported", 3: "CUDA runtime error",
@@ -85,6 +89,12 @@ def lib():
         "cq_quant_rows": (i32, [P, i64, i64, P, P, P]),
         "cq_gemm_a8_workspace_size": (sz, [i64, i64, i64, i32, i32, i32]),
         "cq_gemm_a8": (i32, [P, i64, P, P, P, i64, i64, i32, i32, i32, i32, i32, P, P, sz, P]),
+        "cq_gemm_i8_workspace_size": (sz, [i64, i64, i64, i32]),
+        "cq_gemm_i8": (i32, [P, P, i64, P, P, i64, i64, i32, i32, P, P, sz, P]),
+        "cq_linear_i8": (i32, [P, i64, P, P, i64, i64, i32, i32, P, P, sz, P]),
+        "cq_moe_i8_workspace_size": (sz, [i64, i32, i32, i64, i64]),
+        "cq_moe_i8": (i32, [P, i64, P, P, i32, i32, P, P, P, P, i64, i64, i32, P, P, P, sz, P]),
+        "cq_moe_route": (i32, [P, i32, i64, i32, i32, P, i32, i32, ctypes.c_float, P, P, P]),
         "cq_test_gemm_path": (i32, [P, i64, P, P, P, i64, i64, i32, i32, i32, i32, i32, P, P,
                                     sz, i32, P]),
     }
@@ -346,6 +356,190 @@ def cq_moe_grouped_gemm(tokens, topk_ids, topk_w, layer, E: int, H: int, I: int,
             _ptr(layer), H, I, G, mode, out_dtype, _ptr(ro), _ptr(out), _ptr(workspace),
             workspace.numel(), _stream(stream)), "cq_moe_grouped_gemm")
         return ro, out
+
+
+# ---------------------------------------------------------------------------
+# INT8 weights
+# ---------------------------------------------------------------------------
+_NULL = contextlib.nullcontext()
+
+
+def _on_device(t, stream):
+    """The call's device and stream as the current ones (libcq launches on the
+    current device)."""
+    if t.device.index == torch.cuda.current_device():
+        return _NULL if stream is None else torch.cuda.stream(stream)
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(t.device))
+    if stream is not None:
+        stack.enter_context(torch.cuda.stream(stream))
+    return stack
+
+
+def _tensor(name, t, dtype, shape, device):
+    """Check one argument of a call and return its address."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _scratch(workspace, device):
+    """(address, bytes) of a call's workspace."""
+    if workspace is None:
+        return None, 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous on {device}")
+    n = workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), n
+
+
+def _out_dtype(out_dtype: int):
+    if out_dtype not in (F32, BF16):
+        raise ValueError(f"out_dtype must be F32 or BF16, not {out_dtype!r}")
+    return torch.float32 if out_dtype == F32 else torch.bfloat16
+
+
+def gemm_i8_workspace_size(M, N, K, epilogue=EPI_NONE) -> int:
+    return int(lib().cq_gemm_i8_workspace_size(M, N, K, epilogue))
+
+
+def gemm_i8_workspace(M, N, K, epilogue=EPI_NONE, device="cuda"):
+    """A zero-initialised workspace for cq_gemm_i8 and cq_linear_i8."""
+    n = gemm_i8_workspace_size(M, N, K, epilogue)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def _i8_product(where, x, absmax, wq, wscale, epilogue, out_dtype, out, workspace, stream):
+    if x.dim() != 2 or wq.dim() != 2:
+        raise ValueError(f"{where}: activations [M][K] and weights [N][K] expected")
+    _need_cuda(x)
+    dev = x.device
+    M, K = x.shape
+    N = wq.shape[0]
+    dt = _out_dtype(out_dtype)
+    px = _tensor("xq" if absmax is not None else "x", x,
+                 torch.int8 if absmax is not None else torch.bfloat16, (M, K), dev)
+    pw = _tensor("wq", wq, torch.int8, (N, K), dev)
+    ps = _tensor("wscale", wscale, torch.float32, (N,), dev)
+    shape = (M, N // 2 if epilogue == EPI_SWIGLU else N)
+    with _on_device(x, stream):
+        if out is None:
+            out = torch.empty(shape, dtype=dt, device=dev)
+            py = out.data_ptr()
+        else:
+            py = _tensor("out", out, dt, shape, dev)
+        need = lib().cq_gemm_i8_workspace_size(M, N, K, epilogue)
+        if workspace is None and need:
+            workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+        pws, nws = _scratch(workspace, dev)
+        st = torch.cuda.current_stream().cuda_stream
+        if absmax is not None:
+            pa = _tensor("absmax", absmax, torch.float32, (M,), dev)
+            _check(lib().cq_gemm_i8(px, pa, M, pw, ps, N, K, epilogue, out_dtype, py, pws, nws,
+                                    st), where)
+        else:
+            _check(lib().cq_linear_i8(px, M, pw, ps, N, K, epilogue, out_dtype, py, pws, nws,
+                                      st), where)
+    return out
+
+
+def cq_gemm_i8(xq, absmax, wq, wscale, epilogue: int = EPI_NONE, out_dtype: int = F32, out=None,
+               workspace=None, stream=None):
+    """y = (absmax / 127) wscale (xq wq^T): INT8 activations (cq_quant_rows) times INT8
+    weights [N][K] with one scale per output channel."""
+    if absmax is None:
+        raise ValueError("cq_gemm_i8 needs absmax (cq_quant_rows returns it)")
+    return _i8_product("cq_gemm_i8", xq, absmax, wq, wscale, epilogue, out_dtype, out, workspace,
+                       stream)
+
+
+def cq_linear_i8(x, wq, wscale, epilogue: int = EPI_NONE, out_dtype: int = F32, out=None,
+                 workspace=None, stream=None):
+    """cq_gemm_i8 on bfloat16 activations, quantized per row inside the call."""
+    return _i8_product("cq_linear_i8", x, None, wq, wscale, epilogue, out_dtype, out, workspace,
+                       stream)
+
+
+def moe_i8_workspace_size(T, k, E, H, I) -> int:
+    return int(lib().cq_moe_i8_workspace_size(T, k, E, H, I))
+
+
+def moe_i8_workspace(T, k, E, H, I, device="cuda"):
+    """A zero-initialised workspace for cq_moe_i8."""
+    n = moe_i8_workspace_size(T, k, E, H, I)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def cq_moe_i8(tokens, topk_ids, topk_w, w_gu, s_gu, w_dn, s_dn, out_dtype: int = F32,
+              route_out=True, combine=True, workspace=None, stream=None):
+    """Routed-expert FFN of one MoE layer on INT8 experts, for a few tokens:
+    w_gu int8 [E][2I][H], s_gu [E][2I], w_dn int8 [E][H][I], s_dn [E][H].
+    Returns (route_out, out) as cq_moe_grouped_gemm does."""
+    if tokens.dim() != 2 or topk_ids.dim() != 2 or w_gu.dim() != 3 or w_dn.dim() != 3:
+        raise ValueError("cq_moe_i8: tokens [T][H], topk_ids [T][k], w_gu [E][2I][H] and "
+                         "w_dn [E][H][I] expected")
+    _need_cuda(tokens)
+    dev = tokens.device
+    T, H = tokens.shape
+    k = topk_ids.shape[1]
+    E, _, I = w_dn.shape
+    dt = _out_dtype(out_dtype)
+    pt = _tensor("tokens", tokens, torch.bfloat16, (T, H), dev)
+    pi = _tensor("topk_ids", topk_ids, torch.int32, (T, k), dev)
+    if topk_w is None and combine:
+        raise ValueError("cq_moe_i8 needs topk_w to combine the routes")
+    pk = None if topk_w is None else _tensor("topk_w", topk_w, torch.float32, (T, k), dev)
+    pgu = _tensor("w_gu", w_gu, torch.int8, (E, 2 * I, H), dev)
+    psg = _tensor("s_gu", s_gu, torch.float32, (E, 2 * I), dev)
+    pdn = _tensor("w_dn", w_dn, torch.int8, (E, H, I), dev)
+    psd = _tensor("s_dn", s_dn, torch.float32, (E, H), dev)
+    with _on_device(tokens, stream):
+        ro = pro = None
+        if route_out is True:
+            ro = torch.empty((T * k, H), dtype=torch.float32, device=dev)
+            pro = ro.data_ptr()
+        elif route_out is not None and route_out is not False:
+            ro = route_out
+            pro = _tensor("route_out", ro, torch.float32, (T * k, H), dev)
+        out = po = None
+        if combine:
+            out = torch.empty((T, H), dtype=dt, device=dev)
+            po = out.data_ptr()
+        if workspace is None:
+            workspace = moe_i8_workspace(T, k, E, H, I, dev)
+        pws, nws = _scratch(workspace, dev)
+        _check(lib().cq_moe_i8(pt, T, pi, pk, k, E, pgu, psg, pdn, psd, H, I, out_dtype, pro, po,
+                               pws, nws, torch.cuda.current_stream().cuda_stream), "cq_moe_i8")
+    return ro, out
+
+
+def cq_moe_route(logits, k: int, bias=None, scoring: int = SCORE_SOFTMAX, renorm: bool = True,
+                 scale: float = 1.0, stream=None):
+    """The k experts of each row of router logits [T][E] (float32 or bfloat16):
+    (topk_ids int32 [T][k], topk_w float32 [T][k]), as the MoE layers take them."""
+    if logits.dim() != 2:
+        raise ValueError("cq_moe_route: logits [T][E] expected")
+    _need_cuda(logits)
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"logits are {logits.dtype}, expected float32 or bfloat16")
+    dev = logits.device
+    T, E = logits.shape
+    pl = _tensor("logits", logits, logits.dtype, (T, E), dev)
+    pb = None if bias is None else _tensor("bias", bias, torch.float32, (E,), dev)
+    with _on_device(logits, stream):
+        ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+        w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+        _check(lib().cq_moe_route(pl, BF16 if logits.dtype == torch.bfloat16 else F32, T, E, k,
+                                  pb, scoring, 1 if renorm else 0, scale, ids.data_ptr(),
+                                  w.data_ptr(), torch.cuda.current_stream().cuda_stream),
+               "cq_moe_route")
+    return ids, w
 
 
 def device_error(stream=None) -> tuple[int, int]:

@@ -114,6 +114,25 @@ inline int encode_packed_rows(CUtensorMap* map, const void* base, int64_t rows,
   return r == CUDA_SUCCESS ? CQ_OK : CQ_ERR_CUDA;
 }
 
+// Launch with programmatic dependent launch (the kernel's setup may overlap
+// the end of the preceding kernel; it calls griddep_wait before it reads
+// anything that kernel wrote).
+template <typename... KArgs, typename... Args>
+inline int launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                      cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? CQ_OK : CQ_ERR_CUDA;
+}
+
 inline int num_sms() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;

@@ -5,3 +5,5 @@
 #include "cq_moe.cu"
 #include "cq_noalloc.cu"
 #include "cq_a8.cu"
+#include "cq_i8.cu"
+#include "cq_route.cu"

@@ -1,0 +1,52 @@
+// cq_route.cu -- host side of the MoE router (cq_moe_route).  Part of
+// libcq's single translation unit.
+#include <cuda_runtime.h>
+
+#include "cq.h"
+#include "cq_host.h"
+#include "cq_route.cuh"
+
+namespace cq {
+
+template <int NV>
+static int launch_route(const RouteParams& p, cudaStream_t s) {
+  return launch_pdl(route_topk_kernel<NV>,
+                    dim3(static_cast<unsigned>((p.T + kRtWarps - 1) / kRtWarps)),
+                    dim3(kRtWarps * 32), 0, s, p);
+}
+
+}  // namespace cq
+
+using namespace cq;
+
+extern "C" CQ_API int cq_moe_route(const void* logits, int logits_dtype, int64_t T, int E, int k,
+                                   const float* bias, int scoring, int renorm, float scale,
+                                   int32_t* topk_ids, float* topk_w, void* stream) {
+  if (T < 0 || E <= 0 || k <= 0 || k > E) return CQ_ERR_INVALID_ARG;
+  if (logits_dtype != CQ_DTYPE_F32 && logits_dtype != CQ_DTYPE_BF16) return CQ_ERR_INVALID_ARG;
+  if (scoring != CQ_SCORE_SOFTMAX && scoring != CQ_SCORE_SIGMOID) return CQ_ERR_INVALID_ARG;
+  if (renorm != 0 && renorm != 1) return CQ_ERR_INVALID_ARG;
+  if (E > kRtMaxExperts || k > kRtMaxTopk || T > (int64_t)1 << 31) return CQ_ERR_UNSUPPORTED;
+  if (T == 0) return CQ_OK;
+  if (!logits || !topk_ids || !topk_w) return CQ_ERR_INVALID_ARG;
+  if (!aligned(logits, logits_dtype == CQ_DTYPE_BF16 ? 2 : 4) || !aligned(topk_ids, 4) ||
+      !aligned(topk_w, 4) || (bias && !aligned(bias, 4)))
+    return CQ_ERR_UNSUPPORTED;
+  RouteParams p = {};
+  p.logits = logits;
+  p.bias = bias;
+  p.ids = topk_ids;
+  p.w = topk_w;
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.sigmoid = scoring == CQ_SCORE_SIGMOID;
+  p.renorm = renorm;
+  p.bf16 = logits_dtype == CQ_DTYPE_BF16;
+  p.scale = scale;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // registers for the row's logits: 32 per unit of NV
+  if (E <= 128) return launch_route<4>(p, s);
+  if (E <= 512) return launch_route<16>(p, s);
+  return launch_route<32>(p, s);
+}

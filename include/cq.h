@@ -75,6 +75,7 @@ typedef enum {
 enum { CQ_GRID_MIDRISE = 0, CQ_GRID_MIDTREAD = 1 };
 enum { CQ_DTYPE_F32 = 0, CQ_DTYPE_BF16 = 1 };
 enum { CQ_EPI_NONE = 0, CQ_EPI_SWIGLU = 1 };
+enum { CQ_SCORE_SOFTMAX = 0, CQ_SCORE_SIGMOID = 1 };
 
 /* Library version as 10000*major + 100*minor + patch. */
 CQ_API int cq_version(void);
@@ -301,6 +302,101 @@ CQ_API int cq_moe_grouped_gemm(const uint16_t *tokens, int64_t T, const int32_t 
                                const float *topk_w, int k, int E, const void *layer, int64_t H,
                                int64_t I, int G, int grid_mode, int out_dtype, void *route_out,
                                void *out, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * INT8 weights times INT8 activations (W8A8), for the matrices a checkpoint
+ * keeps in 8 bits beside the CubicQuant experts (shared experts,
+ * projections, whole experts; the pages' layer-wise INT scheme uses it for
+ * them with activations quantized per token):
+ *   xq, absmax  as cq_quant_rows writes them,
+ *   w[n][k]   ~ wscale[n] * wq[n][k]   (cq_quant_rows on the rows of W gives
+ *               wq, and wscale = absmax / 127),
+ *   y[m][n]   = RN(absmax[m] / 127) * wscale[n] * sum_k xq[m][k] wq[n][k].
+ * The integer sums are exact, so results do not depend on how the work is
+ * split and are run-to-run deterministic.
+ *
+ * cq_gemm_i8   -- activations quantized before (one cq_quant_rows serves
+ *                 several products).
+ *   xq int8 [M][K]; absmax float [M]
+ * cq_linear_i8 -- bfloat16 activations, quantized inside the call with the
+ *                 same codes.
+ *   x bfloat16 [M][K]
+ *   wq       int8 [N][K]; wscale float [N]
+ *   epilogue CQ_EPI_NONE: y [M][N]; CQ_EPI_SWIGLU: rows [0,N/2) of W are
+ *            gate, the others up, y is [M][N/2]; requires N even
+ *   y        float or bfloat16 (out_dtype)
+ *   workspace  device scratch of cq_gemm_i8_workspace_size(...) bytes, 256-byte
+ *            aligned (may be NULL when that size is 0), zero before the first
+ *            call that uses it; every completed call leaves its counters zero
+ * K a multiple of 16, at most 131072; M, N at most 2^24; x, wq, y 16-byte
+ * aligned.  |acc| <= 2^31 is exact: 127^2 * 131072 = 2,114,060,288.  A value
+ * of -128 in wq or xq counts as such (and the bound then needs K < 131072).
+ * An infinite activation gives absmax = inf and outputs that are not finite
+ * in its row; NaN activations get code 0 and do not raise absmax.
+ * Calls that share one workspace must not overlap on the GPU.
+ */
+CQ_API size_t cq_gemm_i8_workspace_size(int64_t M, int64_t N, int64_t K, int epilogue);
+CQ_API int cq_gemm_i8(const int8_t *xq, const float *absmax, int64_t M, const int8_t *wq,
+                      const float *wscale, int64_t N, int64_t K, int epilogue, int out_dtype,
+                      void *y, void *workspace, size_t ws_bytes, void *stream);
+CQ_API int cq_linear_i8(const uint16_t *x, int64_t M, const int8_t *wq, const float *wscale,
+                        int64_t N, int64_t K, int epilogue, int out_dtype, void *y,
+                        void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * cq_moe_i8 -- the routed-expert FFN of one MoE layer with INT8 experts, for
+ * a few tokens (a decode step): two kernels that read each expert in use
+ * once.  For every route r = t*k + j with e = topk_ids[t][j]:
+ *   xq, absmax = cq_quant_rows(tokens[t]);
+ *   g|u   = RN(absmax / 127) * s_gu[e][n] * (xq . w_gu[e][n])
+ *   h     = RN32(silu(g) * u), evaluated in FP64 so that the codes of
+ *   hq, hmax = cq_quant_rows(h) (of the FP32 values) do not depend on how it
+ *              is computed;
+ *   y_r   = RN(hmax / 127) * s_dn[e][n] * (hq . w_dn[e][n])
+ * and out[t] = sum_j topk_w[t][j] * y_(t,j) (j ascending, FP32).
+ *   tokens    bfloat16 [T][H]
+ *   topk_ids  int32 [T][k]; an id outside [0, E) drops the route (y_r = 0).
+ *             The same id twice in a token counts twice.
+ *   topk_w    float [T][k] (required when out != NULL; not read for dropped routes)
+ *   w_gu      int8 [E][2I][H], gate rows [0,I), up rows [I,2I); s_gu float [E][2I]
+ *   w_dn      int8 [E][H][I]; s_dn float [E][H]
+ *   route_out float [T*k][H] per-route outputs (may be NULL)
+ *   out       [T][H] in out_dtype (may be NULL)
+ *   workspace device scratch of cq_moe_i8_workspace_size(...) bytes, 256-byte
+ *             aligned, zero before the first call that uses it; every
+ *             completed call leaves its counters zero
+ * A shared expert of the same width is one more expert: id E-1 and weight 1
+ * in an extra column of topk_ids.  H and I multiples of 16, at most 131072;
+ * k at most 1024; E at most 16384.  More than 1024 routes run as successive
+ * groups of tokens, each reading its experts again.  Calls that share one
+ * workspace must not overlap on the GPU.
+ */
+CQ_API size_t cq_moe_i8_workspace_size(int64_t T, int k, int E, int64_t H, int64_t I);
+CQ_API int cq_moe_i8(const uint16_t *tokens, int64_t T, const int32_t *topk_ids,
+                     const float *topk_w, int k, int E, const int8_t *w_gu, const float *s_gu,
+                     const int8_t *w_dn, const float *s_dn, int64_t H, int64_t I, int out_dtype,
+                     float *route_out, void *out, void *workspace, size_t ws_bytes,
+                     void *stream);
+
+/*
+ * cq_moe_route -- a router's logits to the top-k expert ids and weights that
+ * cq_moe_grouped_gemm and cq_moe_i8 take.
+ *   score_e = sigmoid(l_e) (CQ_SCORE_SIGMOID) or softmax(l)_e (CQ_SCORE_SOFTMAX)
+ *   ids     = the k experts of largest score_e + bias_e (bias NULL: of largest
+ *             l_e), in descending order, ties to the lower id.  The sums are
+ *             compared in FP64.
+ *   w_j     = scale * score of ids_j (without the bias); with renorm = 1
+ *             divided by the sum of the k scores (0 where that sum is 0)
+ * An expert whose logit is -inf or NaN, or whose bias is, is never chosen;
+ * slots left without an expert get id -1 and weight 0 (a dropped route).
+ * Equal +inf logits share the softmax.
+ *   logits float or bfloat16 (logits_dtype) [T][E]; bias float [E] or NULL
+ *   topk_ids int32 [T][k]; topk_w float [T][k] (outputs)
+ * E at most 1024, k at most min(E, 32).
+ */
+CQ_API int cq_moe_route(const void *logits, int logits_dtype, int64_t T, int E, int k,
+                        const float *bias, int scoring, int renorm, float scale,
+                        int32_t *topk_ids, float *topk_w, void *stream);
 
 /*
  * cq_get_device_error -- synchronise `stream`, then read and clear the
