@@ -5,6 +5,7 @@
 #include "cq.h"
 #include "cq_host.h"
 #include "cq_i8.cuh"
+#include "cq_i8_tc.cuh"
 
 namespace cq {
 
@@ -61,9 +62,108 @@ static int i8_linear(I8LinearParams p, int sms, cudaStream_t s) {
   return CQ_OK;
 }
 
+// ---------------------------------------------------------------------------
+// the tensor-core product
+// ---------------------------------------------------------------------------
+// Every workspace of the INT8 operators begins with the same counter area,
+// so that one buffer may serve calls of different sizes: counters return to
+// zero, and nothing else is ever written there.
+constexpr size_t kI8CounterBytes = 16384;
+
+struct I8TcPlan {
+  int NT, CG;
+  int n_rt, n_tt, nkb, P;
+  size_t o_xq, o_absmax, o_partial, total;
+};
+
+static size_t i8_round256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Tokens up to which the product is streamed from memory.
+static bool i8_streams(int64_t M) { return M <= kI8MaxTokens; }
+
+static I8TcPlan i8_tc_plan(int64_t M, int64_t N, int64_t K, int epilogue, int sms) {
+  I8TcPlan g;
+  g.NT = M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+  g.CG = g.NT == 256 ? 2 : 1;
+  const int64_t out = epilogue == CQ_EPI_SWIGLU ? N / 2 : N;
+  const int64_t rows = epilogue == CQ_EPI_SWIGLU ? 64 * g.CG : kRows * g.CG;
+  g.n_rt = static_cast<int>((out + rows - 1) / rows);
+  g.n_tt = static_cast<int>((M + g.NT - 1) / g.NT);
+  g.nkb = static_cast<int>((K + kTcBlock - 1) / kTcBlock);
+  const int64_t W = static_cast<int64_t>(g.n_rt) * g.n_tt * g.nkb;
+  const int units = sms / g.CG;
+  g.P = static_cast<int>(W < units ? W : units);
+  g.o_xq = kI8CounterBytes;
+  g.o_absmax = g.o_xq + i8_round256(static_cast<size_t>(M) * K);
+  g.o_partial = g.o_absmax + i8_round256(static_cast<size_t>(M) * sizeof(float));
+  g.total = g.o_partial + static_cast<size_t>(2) * g.P * g.CG * g.NT * kRows * sizeof(int);
+  return g;
+}
+
+// int8 [rows][K] as boxes of 128 bytes x box_rows rows, 128-byte swizzle; with
+// halves == 2, box_rows rows of each half of the rows (gate, then up).
+// Everything outside reads 0.
+static int encode_i8_operand(CUtensorMap* map, const void* base, int64_t rows, int64_t K,
+                             int box_rows, int halves) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return CQ_ERR_CUDA;
+  const cuuint64_t per = static_cast<cuuint64_t>(rows / halves);
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), per, 2};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(K), per * static_cast<cuuint64_t>(K)};
+  cuuint32_t box[3] = {kTcBlock, static_cast<cuuint32_t>(box_rows), 2};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, halves == 2 ? 3u : 2u,
+                  const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? CQ_OK : CQ_ERR_CUDA;
+}
+
+template <int NT, int CG>
+static int launch_i8_tc(const I8TcParams& p, const CUtensorMap& xmap, const CUtensorMap& wmap,
+                        cudaStream_t s) {
+  using C = I8TcCfg<NT, CG>;
+  static std::atomic<uint64_t> smem_set{0};
+  if (!ensure_smem_limit(i8_tc_kernel<NT, CG>, C::SMEM, smem_set)) return CQ_ERR_CUDA;
+  return launch_pdl_cluster(i8_tc_kernel<NT, CG>, dim3(p.P * CG), dim3(kTcThreads), C::SMEM, CG,
+                            s, p, xmap, wmap);
+}
+
+static int i8_tc(const I8LinearParams& q, const I8TcPlan& g, const int8_t* xq,
+                 const float* absmax, uint8_t* ws, cudaStream_t s) {
+  CUtensorMap xmap, wmap;
+  int st = encode_i8_operand(&xmap, xq, q.M, q.K, g.NT / g.CG, 1);
+  if (st != CQ_OK) return st;
+  st = q.swiglu ? encode_i8_operand(&wmap, q.w, q.N, q.K, 16, 2)
+                : encode_i8_operand(&wmap, q.w, q.N, q.K, kRows, 1);
+  if (st != CQ_OK) return st;
+  I8TcParams p = {};
+  p.absmax = absmax;
+  p.wscale = q.wscale;
+  p.y = q.y;
+  p.counter = reinterpret_cast<int*>(ws);
+  p.partial = reinterpret_cast<int*>(ws + g.o_partial);
+  p.M = q.M;
+  p.N = q.N;
+  p.K = q.K;
+  p.swiglu = q.swiglu;
+  p.out_bf16 = q.out_bf16;
+  p.n_rt = g.n_rt;
+  p.n_tt = g.n_tt;
+  p.nkb = g.nkb;
+  p.P = g.P;
+  p.timeout_ns = kDefaultTimeoutNs;
+  switch (g.NT) {
+    case 32: return launch_i8_tc<32, 1>(p, xmap, wmap, s);
+    case 64: return launch_i8_tc<64, 1>(p, xmap, wmap, s);
+    case 128: return launch_i8_tc<128, 1>(p, xmap, wmap, s);
+    default: return launch_i8_tc<256, 2>(p, xmap, wmap, s);
+  }
+}
+
 static int i8_gemm_impl(const void* x, const float* absmax, int64_t M, const int8_t* wq,
                         const float* wscale, int64_t N, int64_t K, int epilogue, int out_dtype,
-                        void* y, bool codes, cudaStream_t s) {
+                        void* y, void* workspace, size_t ws_bytes, bool codes, cudaStream_t s) {
   const int st = validate_i8(M, N, K, epilogue, out_dtype);
   if (st != CQ_OK) return st;
   if (M == 0 || N == 0) return CQ_OK;
@@ -84,7 +184,26 @@ static int i8_gemm_impl(const void* x, const float* absmax, int64_t M, const int
   p.K = static_cast<int>(K);
   p.swiglu = epilogue == CQ_EPI_SWIGLU;
   p.out_bf16 = out_dtype == CQ_DTYPE_BF16;
-  return codes ? i8_linear<I8_SRC_CODES>(p, sms, s) : i8_linear<I8_SRC_BF16>(p, sms, s);
+  if (i8_streams(M))
+    return codes ? i8_linear<I8_SRC_CODES>(p, sms, s) : i8_linear<I8_SRC_BF16>(p, sms, s);
+  const I8TcPlan g = i8_tc_plan(M, N, K, epilogue, sms);
+  if (static_cast<int64_t>(g.n_rt) * g.n_tt >= (int64_t)1 << 31) return CQ_ERR_UNSUPPORTED;
+  if (!workspace) return CQ_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return CQ_ERR_UNSUPPORTED;
+  if (ws_bytes < g.total) return CQ_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int8_t* xq = static_cast<const int8_t*>(x);
+  if (!codes) {
+    int8_t* q = reinterpret_cast<int8_t*>(ws + g.o_xq);
+    float* a = reinterpret_cast<float*>(ws + g.o_absmax);
+    const int e = launch_pdl(quant_rows_vec_kernel, dim3(static_cast<unsigned>(M)),
+                             dim3(kQvThreads), 0, s, static_cast<const uint16_t*>(x), p.M, p.K, q,
+                             a);
+    if (e != CQ_OK) return e;
+    xq = q;
+    absmax = a;
+  }
+  return i8_tc(p, g, xq, absmax, ws, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -95,15 +214,13 @@ struct I8MoePlan {
   size_t o_h, o_y, total;    // the counters come first
 };
 
-static size_t i8_round256(size_t v) { return (v + 255) / 256 * 256; }
-
 static I8MoePlan i8_moe_plan(int64_t T, int k, int64_t H, int64_t I) {
   I8MoePlan m;
   const int64_t most = kI8MaxRoutes / k;
   m.T = T < most ? T : most;
   const size_t R = static_cast<size_t>(m.T) * k;
-  m.o_h = i8_round256(static_cast<size_t>((H + kI8CombineRows - 1) / kI8CombineRows) *
-                      sizeof(int));
+  static_assert(kI8MaxK / kI8CombineRows * sizeof(int) <= kI8CounterBytes, "counter area");
+  m.o_h = kI8CounterBytes;
   m.o_y = m.o_h + i8_round256(R * I * sizeof(float));
   m.total = m.o_y + i8_round256(R * H * sizeof(float));
   return m;
@@ -146,26 +263,27 @@ static int i8_moe_stage(I8MoeParams p, const int8_t* w, const float* wscale, int
 using namespace cq;
 
 extern "C" CQ_API size_t cq_gemm_i8_workspace_size(int64_t M, int64_t N, int64_t K, int epilogue) {
-  (void)M, (void)N, (void)K, (void)epilogue;
-  return 0;
+  if (validate_i8(M, N, K, epilogue, CQ_DTYPE_F32) != CQ_OK || M == 0 || N == 0 || i8_streams(M))
+    return 0;
+  int sms = num_sms();
+  if (sms <= 0) sms = 148;
+  return i8_tc_plan(M, N, K, epilogue, sms).total;
 }
 
 extern "C" CQ_API int cq_gemm_i8(const int8_t* xq, const float* absmax, int64_t M,
                                  const int8_t* wq, const float* wscale, int64_t N, int64_t K,
                                  int epilogue, int out_dtype, void* y, void* workspace,
                                  size_t ws_bytes, void* stream) {
-  (void)workspace, (void)ws_bytes;
-  return i8_gemm_impl(xq, absmax, M, wq, wscale, N, K, epilogue, out_dtype, y, true,
-                      static_cast<cudaStream_t>(stream));
+  return i8_gemm_impl(xq, absmax, M, wq, wscale, N, K, epilogue, out_dtype, y, workspace,
+                      ws_bytes, true, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" CQ_API int cq_linear_i8(const uint16_t* x, int64_t M, const int8_t* wq,
                                    const float* wscale, int64_t N, int64_t K, int epilogue,
                                    int out_dtype, void* y, void* workspace, size_t ws_bytes,
                                    void* stream) {
-  (void)workspace, (void)ws_bytes;
-  return i8_gemm_impl(x, nullptr, M, wq, wscale, N, K, epilogue, out_dtype, y, false,
-                      static_cast<cudaStream_t>(stream));
+  return i8_gemm_impl(x, nullptr, M, wq, wscale, N, K, epilogue, out_dtype, y, workspace,
+                      ws_bytes, false, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" CQ_API size_t cq_moe_i8_workspace_size(int64_t T, int k, int E, int64_t H, int64_t I) {
