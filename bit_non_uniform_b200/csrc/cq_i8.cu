@@ -9,6 +9,7 @@
 
 namespace cq {
 
+constexpr int kI8Devices = 64;            // devices whose properties are remembered
 constexpr int64_t kI8MaxK = 131072;       // one staged row always fits shared memory
 
 // Shared memory left for staged rows beside the accumulators and a kernel's
@@ -65,15 +66,10 @@ static int i8_linear(I8LinearParams p, int sms, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 // the tensor-core product
 // ---------------------------------------------------------------------------
-// Every workspace of the INT8 operators begins with the same counter area,
-// so that one buffer may serve calls of different sizes: counters return to
-// zero, and nothing else is ever written there.
-constexpr size_t kI8CounterBytes = 16384;
-
 struct I8TcPlan {
-  int NT, CG;
-  int n_rt, n_tt, nkb, P;
-  size_t o_xq, o_absmax, o_partial, total;
+  bool pair;
+  int NT, rows, split;       // tokens and weight rows of a CTA's tile, CTAs per tile
+  int n_rt, n_tt, nkb;
 };
 
 static size_t i8_round256(size_t v) { return (v + 255) / 256 * 256; }
@@ -81,83 +77,171 @@ static size_t i8_round256(size_t v) { return (v + 255) / 256 * 256; }
 // Tokens up to which the product is streamed from memory.
 static bool i8_streams(int64_t M) { return M <= kI8MaxTokens; }
 
-static I8TcPlan i8_tc_plan(int64_t M, int64_t N, int64_t K, int epilogue, int sms) {
-  I8TcPlan g;
-  g.NT = M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-  g.CG = g.NT == 256 ? 2 : 1;
-  const int64_t out = epilogue == CQ_EPI_SWIGLU ? N / 2 : N;
-  const int64_t rows = epilogue == CQ_EPI_SWIGLU ? 64 * g.CG : kRows * g.CG;
-  g.n_rt = static_cast<int>((out + rows - 1) / rows);
-  g.n_tt = static_cast<int>((M + g.NT - 1) / g.NT);
-  g.nkb = static_cast<int>((K + kTcBlock - 1) / kTcBlock);
-  const int64_t W = static_cast<int64_t>(g.n_rt) * g.n_tt * g.nkb;
-  const int units = sms / g.CG;
-  g.P = static_cast<int>(W < units ? W : units);
-  g.o_xq = kI8CounterBytes;
-  g.o_absmax = g.o_xq + i8_round256(static_cast<size_t>(M) * K);
-  g.o_partial = g.o_absmax + i8_round256(static_cast<size_t>(M) * sizeof(float));
-  g.total = g.o_partial + static_cast<size_t>(2) * g.P * g.CG * g.NT * kRows * sizeof(int);
-  return g;
+// Clusters of `s` CTAs of the split kernel that run at once (a GPC's SMs need
+// not divide evenly): asked once per device and size.
+static int i8_clusters_at_once(int s, int sms) {
+  static std::atomic<int> known[kI8Devices][kTcMaxSplit + 1];
+  int dev = 0;
+  if (s == 1 || cudaGetDevice(&dev) != cudaSuccess || dev >= kI8Devices) return sms / s;
+  int n = known[dev][s].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  static std::atomic<uint64_t> smem_set{0};
+  if (!ensure_smem_limit(i8_split_kernel<128>, I8SplitCfg<128>::SMEM, smem_set)) return sms / s;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(static_cast<unsigned>(sms / s * s));
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = I8SplitCfg<128>::SMEM;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(s);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, i8_split_kernel<128>, &cfg) != cudaSuccess || n <= 0)
+    return sms / s;
+  known[dev][s].store(n, std::memory_order_relaxed);
+  return n;
 }
 
-// int8 [rows][K] as boxes of 128 bytes x box_rows rows, 128-byte swizzle; with
-// halves == 2, box_rows rows of each half of the rows (gate, then up).
-// Everything outside reads 0.
-static int encode_i8_operand(CUtensorMap* map, const void* base, int64_t rows, int64_t K,
-                             int box_rows, int halves) {
+// Cycles of one K block of a tile: the MMAs (128 rows x nt tokens per SM), or
+// the block's bytes at about 40 per cycle and SM.
+static int64_t i8_block_cost(int nt, int rows_loaded) {
+  const int64_t mma = 2 * nt, bytes = rows_loaded * kTcBlock / 40;
+  return mma > bytes ? mma : bytes;
+}
+
+// The cheapest kernel and tile by an estimate in cycles: rounds of tiles over
+// the SMs x K blocks per CTA x the cost of a block, and a constant for the
+// cluster's sum.
+static I8TcPlan i8_tc_plan(int64_t M, int64_t N, int64_t K, int epilogue, int sms) {
+  const bool sw = epilogue == CQ_EPI_SWIGLU;
+  const int64_t out = sw ? N / 2 : N;
+  const int64_t nkb = (K + kTcBlock - 1) / kTcBlock;
+  I8TcPlan best = {};
+  int64_t cost = INT64_MAX;
+  auto consider = [&](bool pair, int nt, int rows, int split, int64_t n_rt, int64_t n_tt,
+                      int64_t c) {
+    if (c >= cost) return;
+    cost = c;
+    best = {pair, nt, rows, split, static_cast<int>(n_rt), static_cast<int>(n_tt),
+            static_cast<int>(nkb)};
+  };
+  for (int nt = 256; nt >= 128; nt -= 32) {
+    const int64_t per = sw ? kRows : 2 * kRows;
+    const int64_t n_rt = (out + per - 1) / per, n_tt = (M + nt - 1) / nt;
+    const int64_t rounds = (n_rt * n_tt + sms / 2 - 1) / (sms / 2);
+    consider(true, nt, kRows, 1, n_rt, n_tt,
+             rounds * nkb * i8_block_cost(nt, kRows + nt / 2) + 6000);
+  }
+  for (int nt = 32; nt <= 128; nt *= 2) {
+    for (int rows = kRows; rows >= 32; rows -= 16) {
+      const int64_t per = sw ? rows / 2 : rows;
+      const int64_t n_rt = (out + per - 1) / per, n_tt = (M + nt - 1) / nt;
+      for (int s = 1; s <= kTcMaxSplit && s <= nkb; ++s) {
+        const int at_once = i8_clusters_at_once(s, sms);
+        const int64_t rounds = (n_rt * n_tt + at_once - 1) / at_once;
+        const int64_t each =
+            (nkb + s - 1) / s * i8_block_cost(nt, rows + nt) + 3000 + (s > 1 ? 2000 : 0);
+        consider(false, nt, rows, s, n_rt, n_tt, rounds * each);
+      }
+    }
+  }
+  return best;
+}
+
+static int i8_encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+                     const cuuint64_t* strides, const cuuint32_t* box) {
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return CQ_ERR_CUDA;
-  const cuuint64_t per = static_cast<cuuint64_t>(rows / halves);
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), per, 2};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(K), per * static_cast<cuuint64_t>(K)};
-  cuuint32_t box[3] = {kTcBlock, static_cast<cuuint32_t>(box_rows), 2};
-  cuuint32_t estr[3] = {1u, 1u, 1u};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, halves == 2 ? 3u : 2u,
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank),
                   const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? CQ_OK : CQ_ERR_CUDA;
 }
 
-template <int NT, int CG>
-static int launch_i8_tc(const I8TcParams& p, const CUtensorMap& xmap, const CUtensorMap& wmap,
-                        cudaStream_t s) {
-  using C = I8TcCfg<NT, CG>;
+// int8 [rows][K] as boxes of 128 bytes x box_rows rows, 128-byte swizzle.
+// Everything outside reads 0.
+static int encode_i8_rows(CUtensorMap* map, const void* base, int64_t rows, int64_t K,
+                          int box_rows) {
+  const cuuint64_t k = static_cast<cuuint64_t>(K);
+  const cuuint64_t dims[2] = {k, static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {k};
+  const cuuint32_t box[2] = {kTcBlock, static_cast<cuuint32_t>(box_rows)};
+  return i8_encode(map, base, 2, dims, strides, box);
+}
+
+// Gate and up rows (each `out` of them) in alternating groups of 8: 8 rows of
+// both halves per box, and `groups` of these (groups == 0: a map for one at a
+// time, which also takes `out` that is not a multiple of 8).
+static int encode_i8_gate_up(CUtensorMap* map, const void* base, int64_t out, int64_t K,
+                             int groups) {
+  const cuuint64_t k = static_cast<cuuint64_t>(K), h = static_cast<cuuint64_t>(out);
+  if (groups == 0) {
+    const cuuint64_t dims[3] = {k, h, 2};
+    const cuuint64_t strides[2] = {k, h * k};
+    const cuuint32_t box[3] = {kTcBlock, 8, 2};
+    return i8_encode(map, base, 3, dims, strides, box);
+  }
+  const cuuint64_t dims[4] = {k, 8, 2, h / 8};
+  const cuuint64_t strides[3] = {k, h * k, 8 * k};
+  const cuuint32_t box[4] = {kTcBlock, 8, 2, static_cast<cuuint32_t>(groups)};
+  return i8_encode(map, base, 4, dims, strides, box);
+}
+
+template <int NT>
+static int launch_i8_split(const I8TcParams& p, const CUtensorMap& xmap, const CUtensorMap& wmap,
+                           cudaStream_t s) {
   static std::atomic<uint64_t> smem_set{0};
-  if (!ensure_smem_limit(i8_tc_kernel<NT, CG>, C::SMEM, smem_set)) return CQ_ERR_CUDA;
-  return launch_pdl_cluster(i8_tc_kernel<NT, CG>, dim3(p.P * CG), dim3(kTcThreads), C::SMEM, CG,
-                            s, p, xmap, wmap);
+  if (!ensure_smem_limit(i8_split_kernel<NT>, I8SplitCfg<NT>::SMEM, smem_set)) return CQ_ERR_CUDA;
+  return launch_pdl_cluster(i8_split_kernel<NT>,
+                            dim3(static_cast<unsigned>(p.n_rt * p.n_tt * p.split)),
+                            dim3(kTcThreads), I8SplitCfg<NT>::SMEM, p.split, s, p, xmap, wmap);
+}
+
+static int launch_i8_pair(const I8TcParams& p, const CUtensorMap& xmap, const CUtensorMap& wmap,
+                          int sms, cudaStream_t s) {
+  static std::atomic<uint64_t> smem_set{0};
+  if (!ensure_smem_limit(i8_pair_kernel, I8PairCfg::SMEM, smem_set)) return CQ_ERR_CUDA;
+  const int tiles = p.n_rt * p.n_tt, units = sms / 2;
+  return launch_pdl_cluster(i8_pair_kernel, dim3(2u * (tiles < units ? tiles : units)),
+                            dim3(kTcThreads), I8PairCfg::SMEM, 2, s, p, xmap, wmap);
 }
 
 static int i8_tc(const I8LinearParams& q, const I8TcPlan& g, const int8_t* xq,
-                 const float* absmax, uint8_t* ws, cudaStream_t s) {
+                 const float* absmax, bool early_w, int sms, cudaStream_t s) {
   CUtensorMap xmap, wmap;
-  int st = encode_i8_operand(&xmap, xq, q.M, q.K, g.NT / g.CG, 1);
+  int st = encode_i8_rows(&xmap, xq, q.M, q.K, g.pair ? g.NT / 2 : g.NT);
   if (st != CQ_OK) return st;
-  st = q.swiglu ? encode_i8_operand(&wmap, q.w, q.N, q.K, 16, 2)
-                : encode_i8_operand(&wmap, q.w, q.N, q.K, kRows, 1);
+  const int64_t half = q.N / 2;
+  const bool one_box = q.swiglu && half % 8 == 0;
+  st = !q.swiglu ? encode_i8_rows(&wmap, q.w, q.N, q.K, g.rows)
+                 : encode_i8_gate_up(&wmap, q.w, half, q.K, one_box ? g.rows / 16 : 0);
   if (st != CQ_OK) return st;
   I8TcParams p = {};
   p.absmax = absmax;
   p.wscale = q.wscale;
   p.y = q.y;
-  p.counter = reinterpret_cast<int*>(ws);
-  p.partial = reinterpret_cast<int*>(ws + g.o_partial);
   p.M = q.M;
   p.N = q.N;
-  p.K = q.K;
   p.swiglu = q.swiglu;
   p.out_bf16 = q.out_bf16;
   p.n_rt = g.n_rt;
   p.n_tt = g.n_tt;
   p.nkb = g.nkb;
-  p.P = g.P;
+  p.split = g.split;
+  p.rows = g.rows;
+  p.w_boxes = one_box ? 1 : g.rows / 16;
+  p.nt = g.NT;
+  p.early_w = early_w;
   p.timeout_ns = kDefaultTimeoutNs;
+  if (g.pair) return launch_i8_pair(p, xmap, wmap, sms, s);
   switch (g.NT) {
-    case 32: return launch_i8_tc<32, 1>(p, xmap, wmap, s);
-    case 64: return launch_i8_tc<64, 1>(p, xmap, wmap, s);
-    case 128: return launch_i8_tc<128, 1>(p, xmap, wmap, s);
-    default: return launch_i8_tc<256, 2>(p, xmap, wmap, s);
+    case 32: return launch_i8_split<32>(p, xmap, wmap, s);
+    case 64: return launch_i8_split<64>(p, xmap, wmap, s);
+    default: return launch_i8_split<128>(p, xmap, wmap, s);
   }
 }
 
@@ -187,15 +271,16 @@ static int i8_gemm_impl(const void* x, const float* absmax, int64_t M, const int
   if (i8_streams(M))
     return codes ? i8_linear<I8_SRC_CODES>(p, sms, s) : i8_linear<I8_SRC_BF16>(p, sms, s);
   const I8TcPlan g = i8_tc_plan(M, N, K, epilogue, sms);
-  if (static_cast<int64_t>(g.n_rt) * g.n_tt >= (int64_t)1 << 31) return CQ_ERR_UNSUPPORTED;
-  if (!workspace) return CQ_ERR_WORKSPACE;
-  if (!aligned(workspace, 256)) return CQ_ERR_UNSUPPORTED;
-  if (ws_bytes < g.total) return CQ_ERR_WORKSPACE;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (static_cast<int64_t>(g.n_rt) * g.n_tt * g.split >= (int64_t)1 << 30)
+    return CQ_ERR_UNSUPPORTED;
   const int8_t* xq = static_cast<const int8_t*>(x);
   if (!codes) {
-    int8_t* q = reinterpret_cast<int8_t*>(ws + g.o_xq);
-    float* a = reinterpret_cast<float*>(ws + g.o_absmax);
+    const size_t o_absmax = i8_round256(static_cast<size_t>(M) * K);
+    if (!workspace || ws_bytes < o_absmax + static_cast<size_t>(M) * sizeof(float))
+      return CQ_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return CQ_ERR_UNSUPPORTED;
+    int8_t* q = static_cast<int8_t*>(workspace);
+    float* a = reinterpret_cast<float*>(q + o_absmax);
     const int e = launch_pdl(quant_rows_vec_kernel, dim3(static_cast<unsigned>(M)),
                              dim3(kQvThreads), 0, s, static_cast<const uint16_t*>(x), p.M, p.K, q,
                              a);
@@ -203,7 +288,9 @@ static int i8_gemm_impl(const void* x, const float* absmax, int64_t M, const int
     xq = q;
     absmax = a;
   }
-  return i8_tc(p, g, xq, absmax, ws, s);
+  // behind the quantization the weights may be fetched early: it ends only
+  // after the kernel before it
+  return i8_tc(p, g, xq, absmax, !codes, sms, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -219,8 +306,9 @@ static I8MoePlan i8_moe_plan(int64_t T, int k, int64_t H, int64_t I) {
   const int64_t most = kI8MaxRoutes / k;
   m.T = T < most ? T : most;
   const size_t R = static_cast<size_t>(m.T) * k;
-  static_assert(kI8MaxK / kI8CombineRows * sizeof(int) <= kI8CounterBytes, "counter area");
-  m.o_h = kI8CounterBytes;
+  // a fixed area for the counters, so that one buffer may serve layers of
+  // different sizes: counters return to zero, and nothing else is written there
+  m.o_h = kI8MaxK / kI8CombineRows * sizeof(int);
   m.o_y = m.o_h + i8_round256(R * I * sizeof(float));
   m.total = m.o_y + i8_round256(R * H * sizeof(float));
   return m;
@@ -265,9 +353,7 @@ using namespace cq;
 extern "C" CQ_API size_t cq_gemm_i8_workspace_size(int64_t M, int64_t N, int64_t K, int epilogue) {
   if (validate_i8(M, N, K, epilogue, CQ_DTYPE_F32) != CQ_OK || M == 0 || N == 0 || i8_streams(M))
     return 0;
-  int sms = num_sms();
-  if (sms <= 0) sms = 148;
-  return i8_tc_plan(M, N, K, epilogue, sms).total;
+  return i8_round256(static_cast<size_t>(M) * K) + i8_round256(static_cast<size_t>(M) * sizeof(float));
 }
 
 extern "C" CQ_API int cq_gemm_i8(const int8_t* xq, const float* absmax, int64_t M,

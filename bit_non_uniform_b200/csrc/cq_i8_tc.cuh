@@ -1,33 +1,43 @@
 // cq_i8_tc.cuh -- INT8 weights times INT8 activations on the tensor cores
 // (tcgen05.mma kind::i8), for more tokens than the streamed product takes.
 //
-// A tile is 128 CG weight rows (the MMA's M) x NT tokens (its N).  Both
-// operands come from shared memory, K-major with the 128-byte swizzle, loaded
-// by TMA in blocks of 128 bytes of K; the INT32 accumulators live in tensor
-// memory, two buffers, so that a tile's epilogue overlaps the next tile's
-// MMAs.  With CG = 2 a cluster of two CTAs computes one 256 x NT tile
-// (cta_group::2): each CTA loads its 128 weight rows and half of the tokens,
-// which halves the activation traffic and the shared-memory reads per MMA.
-// The launch's work is the list of (tile, K block) pairs split evenly over
-// the CTAs (or pairs); a tile cut by that split is summed from INT32 partial
-// tiles by whichever of its CTAs finishes last (integers: the same result in
-// any order).
+// Operand A is 128 weight rows per CTA, operand B the tokens.  Both come from
+// shared memory, K-major with the 128-byte swizzle, loaded by TMA in blocks
+// of 128 bytes of K; the INT32 accumulators live in tensor memory.
+// Two kernels, chosen by a cost estimate on the host:
+//   * i8_split_kernel: one tile of up to 128 rows x NT tokens per cluster, K
+//     split over the cluster's CTAs (1 to 8).  The MMA always covers 128 rows;
+//     a tile of fewer loads fewer and ignores the others' sums.  For few tokens or few tiles: weights are
+//     read by all SMs although there are fewer tiles than SMs, and the INT32
+//     parts are summed through distributed shared memory, each CTA finishing
+//     its share of the columns.  (A first version split the K blocks of the
+//     persistent kernel over the CTAs and summed partial tiles from global
+//     memory: 105 us instead of 20 at 256 tokens of 6144 x 7168, the last CTA
+//     of each tile reading the parts with 128 threads.)
+//   * i8_pair_kernel: persistent CTA pairs, 256 weight rows x NT tokens per
+//     tile (cta_group::2): each CTA loads its 128 weight rows and half of the
+//     tokens, which halves the activation traffic and the shared-memory reads
+//     per MMA.  Two accumulators, so that a tile's epilogue overlaps the next
+//     tile's MMAs.
 //
-// With SwiGLU a CTA's 128 rows are 16 gate rows, the 16 up rows that belong
-// to them, the next 16 gate rows, and so on, so that gate and up of one
-// output sit in the same warp of the epilogue, 16 lanes apart.
+// With SwiGLU a CTA's rows are 8 gate rows, the 8 up rows that belong to
+// them, the next 8 gate rows, and so on, so that gate and up of one output
+// sit in the same warp of the epilogue, 8 lanes apart.
 //
-// Warp roles (192 threads): warps 0-3 epilogue (TMEM lanes 32 w .. 32 w + 31
-// belong to warp w), warp 4 producer, warp 5 MMA issue and TMEM.
+// Warp roles (320 threads): warps 0-7 epilogue (warps w and w + 4 share TMEM
+// lanes 32 w .. 32 w + 31, 16 columns each in turn; with four warps the
+// epilogue of 128 columns alone took 4 us), warp 8 producer, warp 9 MMA issue
+// and TMEM.
 #pragma once
 
 #include "cq_i8.cuh"
 
 namespace cq {
 
-constexpr int kTcThreads = 192;
-constexpr int kTcProducer = 4;
-constexpr int kTcMma = 5;
+constexpr int kTcThreads = 320;
+constexpr int kTcEpilogue = 256;
+constexpr int kTcProducer = 8;
+constexpr int kTcMma = 9;
 constexpr int kTcBlock = 128;              // bytes of K per stage
 
 enum I8TcSite : int {
@@ -54,6 +64,14 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+__device__ __forceinline__ int4 ld_cluster_int4(uint32_t cluster_ptr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(cluster_ptr)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
                : "memory");
@@ -75,6 +93,16 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap* map, int32_t c0,
+                                                 int32_t c1, int32_t c2, int32_t c3,
+                                                 uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
 }
 
@@ -132,45 +160,368 @@ __device__ __forceinline__ void tc_dealloc(uint32_t addr, uint32_t cols) {
                  : "memory");
 }
 
-template <int NT, int CG>
-struct I8TcCfg {
-  static constexpr int A_BYTES = kRows * kTcBlock;             // this CTA's weight rows
-  static constexpr int B_ROWS = NT / CG;                       // this CTA's tokens
-  static constexpr int B_BYTES = B_ROWS * kTcBlock;
-  static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int MISC = 1024 + NT * 4;                   // barriers, scales
-  static constexpr int RAW = (220 * 1024 - 1024 - MISC) / STAGE;
-  static constexpr int STAGES = RAW > 8 ? 8 : RAW;
-  static constexpr int SMEM = 1024 + STAGES * STAGE + MISC;
-  static constexpr int TMEM = 2 * NT < 32 ? 32 : 2 * NT;       // two accumulators
-  static_assert(STAGES >= 4, "too few stages");
-  static_assert(TMEM <= kTmemCols && (TMEM & (TMEM - 1)) == 0, "TMEM columns");
-  static_assert(STAGE % 1024 == 0 && B_ROWS % 8 == 0, "swizzle atoms");
-};
+constexpr int kTcMaxSplit = 8;
 
 struct I8TcParams {
   const float* absmax;      // [M]
   const float* wscale;      // [N]
   void* y;
-  int* counter;             // [P * CG], zero between launches
-  int* partial;             // [2 P CG][NT][128]
-  int M, N, K;
+  int M, N;
   int swiglu, out_bf16;
-  int n_rt, n_tt, nkb, P;   // row tiles, token tiles, K blocks, CTAs or pairs
+  int n_rt, n_tt, nkb;      // row tiles, token tiles, K blocks
+  int split;                // CTAs per tile (i8_split_kernel)
+  int rows;                 // weight rows per CTA, a multiple of 16
+  int w_boxes;              // SwiGLU: boxes per block of K (1, or rows / 16)
+  int nt;                   // tokens per tile (i8_pair_kernel)
+  int early_w;              // the weights may be read before griddep_wait
   uint64_t timeout_ns;
 };
 
-template <int NT, int CG>
+// AND-vote and barrier of the epilogue's threads.
+__device__ __forceinline__ bool tc_epilogue_vote(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 3, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return r != 0;
+}
+
+// A thread's place in a tile of the epilogue.
+struct I8Lane {
+  int row;                  // TMEM lane
+  int half;                 // takes the 16-column chunks of this parity
+  int col;                  // output column
+  int cols;                 // output columns of y
+  int m0, mv;               // first token, valid tokens
+  bool live;
+  float ws;
+};
+
+// `rt0` is the first output column of this CTA's 128 weight rows.
+__device__ __forceinline__ I8Lane i8_lane(const I8TcParams& p, int rt0, int m0, int nt) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  I8Lane l;
+  l.row = (warp & 3) * 32 + lane;
+  l.half = warp >> 2;
+  l.cols = p.swiglu ? p.N / 2 : p.N;
+  l.m0 = m0;
+  l.mv = p.M - m0 < nt ? p.M - m0 : nt;
+  l.col = rt0 + (p.swiglu ? (l.row >> 4) * 8 + (lane & 7) : l.row);
+  l.live = l.col < l.cols && l.row < p.rows;
+  const int wrow = p.swiglu && (lane & 8) ? l.cols + l.col : l.col;
+  l.ws = l.live ? __ldg(p.wscale + wrow) : 0.f;
+  return l;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void i8_put(uint8_t* at, float v) {
+  if constexpr (BF16)
+    *reinterpret_cast<uint16_t*>(at) = bf16_bits(v);
+  else
+    *reinterpret_cast<float*>(at) = v;
+}
+
+// Scale, SwiGLU and store NQ accumulator columns (tokens m0 + c0 ...) of the
+// lane's row; all 32 lanes call it.
+template <int NQ, bool BF16>
+__device__ __forceinline__ void i8_finish_as(const I8TcParams& p, const I8Lane& l,
+                                             const float* s_sx, const int (&a)[NQ], int c0) {
+  constexpr int ES = BF16 ? 2 : 4;
+  float v[NQ];
+#pragma unroll
+  for (int q = 0; q < NQ; q += 4) {
+    const float4 sx = *reinterpret_cast<const float4*>(s_sx + c0 + q);
+    v[q] = __fmul_rn(__fmul_rn(sx.x, l.ws), static_cast<float>(a[q]));
+    v[q + 1] = __fmul_rn(__fmul_rn(sx.y, l.ws), static_cast<float>(a[q + 1]));
+    v[q + 2] = __fmul_rn(__fmul_rn(sx.z, l.ws), static_cast<float>(a[q + 2]));
+    v[q + 3] = __fmul_rn(__fmul_rn(sx.w, l.ws), static_cast<float>(a[q + 3]));
+  }
+  const int left = l.live ? l.mv - c0 : 0;                  // columns to store
+  const int64_t pitch = static_cast<int64_t>(l.cols) * ES;
+  uint8_t* at = static_cast<uint8_t*>(p.y) + (l.m0 + c0) * pitch + static_cast<int64_t>(l.col) * ES;
+  if (p.swiglu) {
+    // lanes 0-7 hold gate and lanes 8-15 up of the same outputs (16-31
+    // likewise); of two columns the gate lanes take the first, the up lanes
+    // the second
+    const int hi = (threadIdx.x >> 3) & 1;
+    at += hi * pitch;
+#pragma unroll
+    for (int q = 0; q < NQ; q += 2) {
+      const float other = __shfl_xor_sync(0xffffffffu, hi ? v[q] : v[q + 1], 8);
+      const float h = hi ? i8_swiglu_f32(other, v[q + 1]) : i8_swiglu_f32(v[q], other);
+      if (q + hi < left) i8_put<BF16>(at, h);
+      at += 2 * pitch;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      if (q < left) i8_put<BF16>(at, v[q]);
+      at += pitch;
+    }
+  }
+}
+
+template <int NQ>
+__device__ __forceinline__ void i8_finish(const I8TcParams& p, const I8Lane& l, const float* s_sx,
+                                          const int (&a)[NQ], int c0) {
+  if (p.out_bf16)
+    i8_finish_as<NQ, true>(p, l, s_sx, a, c0);
+  else
+    i8_finish_as<NQ, false>(p, l, s_sx, a, c0);
+}
+
+// The tokens' RN(absmax / 127) of a tile, by the epilogue's threads.
+__device__ __forceinline__ void i8_load_scales(const I8TcParams& p, int m0, int mv, int nt,
+                                               float* s_sx) {
+  for (int c = threadIdx.x; c < nt; c += kTcEpilogue)
+    s_sx[c] = c < mv ? __fdiv_rn(__ldg(p.absmax + m0 + c), 127.0f) : 0.f;
+}
+
+// Load this CTA's weight rows of one block of K.  SwiGLU: the tensor map's
+// boxes hold 8 gate rows and the 8 up rows of the same outputs; all of them in
+// one copy (a fourth dimension counts the groups of 8) where the outputs are a
+// multiple of 8, else one copy each (rows past the outputs must read as zero).
+template <bool PAIR>
+__device__ __forceinline__ void i8_load_w(const I8TcParams& p, uint32_t dst,
+                                          const CUtensorMap* map, int k0, int rt0, uint32_t bar) {
+  if (!p.swiglu) {
+    if constexpr (PAIR) tma_load_2d_pair(dst, map, k0, rt0, bar);
+    else tma_load_2d(dst, map, k0, rt0, bar);
+  } else if (p.w_boxes == 1) {
+    if constexpr (PAIR) tma_load_4d_pair(dst, map, k0, 0, 0, rt0 / 8, bar);
+    else tma_load_4d(dst, map, k0, 0, 0, rt0 / 8, bar);
+  } else {
+    for (int q = 0; q < p.w_boxes; ++q) {
+      if constexpr (PAIR) tma_load_3d_pair(dst + q * 2048, map, k0, rt0 + q * 8, 0, bar);
+      else tma_load_3d(dst + q * 2048, map, k0, rt0 + q * 8, 0, bar);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// one tile per cluster, K split over its CTAs
+// ---------------------------------------------------------------------------
+template <int NT>
+struct I8SplitCfg {
+  static constexpr int A_BYTES = kRows * kTcBlock;
+  static constexpr int STAGE = A_BYTES + NT * kTcBlock;
+  static constexpr int MISC = 1024 + NT * 4;
+  static constexpr int RAW = (220 * 1024 - 1024 - MISC) / STAGE;
+  static constexpr int STAGES = RAW > 10 ? 10 : RAW;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + MISC;
+  static constexpr int DUMP = NT * kRows * 4;                  // the accumulator, over the stages
+  static_assert(STAGES >= 4 && DUMP <= STAGES * STAGE && STAGE % 1024 == 0, "shared memory");
+  static_assert(NT >= 32 && NT <= 128 && (NT & (NT - 1)) == 0, "TMEM columns");
+};
+
+template <int NT>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    i8_tc_kernel(const __grid_constant__ I8TcParams p, const __grid_constant__ CUtensorMap xmap,
-                 const __grid_constant__ CUtensorMap wmap) {
-  using C = I8TcCfg<NT, CG>;
+    i8_split_kernel(const __grid_constant__ I8TcParams p, const __grid_constant__ CUtensorMap xmap,
+                    const __grid_constant__ CUtensorMap wmap) {
+  using C = I8SplitCfg<NT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - raw);
   const uint32_t misc = base + C::STAGES * C::STAGE;
-  const uint32_t bar_full = misc;                           // pair: the leader's counts both
+  const uint32_t bar_full = misc;
+  const uint32_t bar_empty = bar_full + 8 * C::STAGES;
+  const uint32_t bar_dfull = bar_empty + 8 * C::STAGES;
+  const uint32_t slot_tmem = bar_dfull + 8;
+  volatile int* const abort_flag =
+      reinterpret_cast<volatile int*>(gbase + (slot_tmem + 8 - base));
+  float* const s_sx = reinterpret_cast<float*>(gbase + (misc + 1024 - base));   // [NT]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int S = p.split;
+  const int tile = static_cast<int>(blockIdx.x) / S;
+  const int part = static_cast<int>(blockIdx.x) - tile * S;   // = rank in the cluster
+  const int tt = tile / p.n_rt, rt = tile - tt * p.n_rt;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(part) * p.nkb / S);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(part + 1) * p.nkb / S);
+  const int rt0 = rt * (p.swiglu ? p.rows / 2 : p.rows);
+  const uint64_t tmo = p.timeout_ns;
+
+  if (tid == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    mbar_init(bar_dfull, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kTcMma) {
+    tc_alloc<1>(slot_tmem, NT);
+    tc_fence_before();
+  }
+  if (warp == kTcProducer && lane == 0) {
+    prefetch_tensormap(&xmap);
+    prefetch_tensormap(&wmap);
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base =
+      *reinterpret_cast<volatile uint32_t*>(gbase + (slot_tmem - base));
+
+  bool ok = true;
+  I8Lane l = {};
+  if (warp == kTcProducer) {
+    if (lane == 0) {
+      const uint32_t bytes = static_cast<uint32_t>(p.rows + NT) * kTcBlock;
+      auto load_w = [&](int kb, int st) {
+        mbar_arrive_expect_tx(bar_full + 8 * st, bytes);
+        i8_load_w<false>(p, base + st * C::STAGE, &wmap, kb * kTcBlock, rt0, bar_full + 8 * st);
+      };
+      // weights no preceding kernel writes are fetched while it ends
+      int early = 0;
+      if (p.early_w) {
+        for (; early < C::STAGES && kb0 + early < kb1; ++early) load_w(kb0 + early, early);
+      }
+      griddep_wait();
+      int st = 0, loads = 0;
+      uint32_t round = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (loads >= early) {
+          if (!wait_phase(bar_empty + 8 * st, (round & 1u) ^ 1u, abort_flag, tmo,
+                          SITE_I8_EMPTY))
+            break;
+          load_w(kb, st);
+        }
+        tma_load_2d(base + st * C::STAGE + C::A_BYTES, &xmap, kb * kTcBlock, tt * NT,
+                    bar_full + 8 * st);
+        ++loads;
+        if (++st == C::STAGES) {
+          st = 0;
+          ++round;
+        }
+      }
+      if (*abort_flag) {
+        // the copies in flight must land before the CTA ends
+        const int armed = loads < C::STAGES ? loads : C::STAGES;
+        for (int k = 1; k <= armed; ++k) {
+          const int idx = loads - k;
+          volatile int dummy = 0;
+          mbar_wait(bar_full + 8 * (idx % C::STAGES),
+                    static_cast<uint32_t>(idx / C::STAGES) & 1u, &dummy, tmo, SITE_TEARDOWN);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kTcMma) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_s8_s32(kRows, NT);
+      int st = 0;
+      uint32_t round = 0, acc = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait_phase(bar_full + 8 * st, round & 1u, abort_flag, tmo, SITE_I8_FULL)) break;
+        tc_fence_after();
+        const uint64_t da = smem_desc_sw128(base + st * C::STAGE);
+        const uint64_t db = smem_desc_sw128(base + st * C::STAGE + C::A_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          mma_ss_i8<1>(tmem_base, da + 2 * kk, db + 2 * kk, idesc, acc);   // 32 bytes each
+          acc = 1;
+        }
+        tc_commit<1>(bar_empty + 8 * st);
+        if (++st == C::STAGES) {
+          st = 0;
+          ++round;
+        }
+      }
+      tc_commit<1>(bar_dfull);
+      volatile int dummy = 0;
+      mbar_wait(bar_dfull, 0, &dummy, tmo, SITE_TEARDOWN);
+    }
+    __syncwarp();
+  } else {
+    griddep_wait();
+    l = i8_lane(p, rt0, tt * NT, NT);
+    i8_load_scales(p, l.m0, l.mv, NT, s_sx);
+    ok = wait_phase(bar_dfull, 0, abort_flag, tmo, SITE_I8_DFULL);
+    ok = tc_epilogue_vote(ok) && *abort_flag == 0;         // also orders s_sx
+    tc_fence_after();
+    const uint32_t daddr = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    int4* const dump = reinterpret_cast<int4*>(gbase);      // [NT / 4][128]
+    for (int cc = l.half; cc * 16 < l.mv; cc += 2) {
+      uint32_t r[16];
+      tmem_ld16(daddr + cc * 16, r);
+      tmem_wait_ld();
+      if (S == 1) {
+        int a[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) a[q] = static_cast<int>(r[q]);
+        if (ok) i8_finish<16>(p, l, s_sx, a, cc * 16);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          dump[(cc * 4 + q) * kRows + l.row] =
+              make_int4(static_cast<int>(r[4 * q]), static_cast<int>(r[4 * q + 1]),
+                        static_cast<int>(r[4 * q + 2]), static_cast<int>(r[4 * q + 3]));
+      }
+    }
+    tc_fence_before();
+  }
+  griddep_launch_dependents();
+  __syncthreads();
+  if (warp == kTcMma) {
+    tc_fence_after();
+    tc_dealloc<1>(tmem_base, NT);
+  }
+  if (S > 1) {
+    __syncwarp();
+    cluster_sync_all();
+    if (warp < kTcProducer && ok) {
+      // columns in quads, dealt out over the cluster's CTAs
+      for (int q = part + S * l.half; q * 4 < l.mv; q += 2 * S) {
+        int a[4] = {0, 0, 0, 0};
+        const uint32_t at = base + static_cast<uint32_t>(q * kRows + l.row) * 16u;
+#pragma unroll
+        for (int c = 0; c < kTcMaxSplit; ++c) {
+          if (c < S) {
+            const int4 v = ld_cluster_int4(cluster_addr(at, c));
+            a[0] += v.x;
+            a[1] += v.y;
+            a[2] += v.z;
+            a[3] += v.w;
+          }
+        }
+        i8_finish<4>(p, l, s_sx, a, q * 4);
+      }
+    }
+    cluster_sync_all();                    // nobody leaves while its parts are read
+  }
+}
+
+// ---------------------------------------------------------------------------
+// persistent CTA pairs
+// ---------------------------------------------------------------------------
+struct I8PairCfg {
+  static constexpr int NT = 256;                               // tokens per tile, at most
+  static constexpr int A_BYTES = kRows * kTcBlock;             // this CTA's weight rows
+  static constexpr int B_BYTES = NT / 2 * kTcBlock;            // this CTA's tokens, at most
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int STAGES = 6;
+  static constexpr int MISC = 1024 + NT * 4;                   // barriers, scales
+  static constexpr int SMEM = 1024 + STAGES * STAGE + MISC;
+  static_assert(SMEM <= 227 * 1024 && 2 * NT <= kTmemCols, "budgets");
+};
+
+__global__ void __launch_bounds__(kTcThreads, 1)
+    i8_pair_kernel(const __grid_constant__ I8TcParams p, const __grid_constant__ CUtensorMap xmap,
+                   const __grid_constant__ CUtensorMap wmap) {
+  using C = I8PairCfg;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const gbase = smem_raw + (base - raw);
+  const uint32_t misc = base + C::STAGES * C::STAGE;
+  const uint32_t bar_full = misc;                           // the leader's count both CTAs' copies
   const uint32_t bar_empty = bar_full + 8 * C::STAGES;
   const uint32_t bar_dfull = bar_empty + 8 * C::STAGES;     // [2]
   const uint32_t bar_dfree = bar_dfull + 16;                // [2], the leader's
@@ -178,13 +529,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t slot_tmem = bar_fin + 8;
   volatile int* const abort_flag =
       reinterpret_cast<volatile int*>(gbase + (slot_tmem + 8 - base));
-  volatile int* const last_flag =
-      reinterpret_cast<volatile int*>(gbase + (slot_tmem + 12 - base));
   float* const s_sx = reinterpret_cast<float*>(gbase + (misc + 1024 - base));   // [NT]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
-  const int unit = CG == 2 ? static_cast<int>(blockIdx.x) >> 1 : static_cast<int>(blockIdx.x);
+  const int rank = static_cast<int>(cluster_rank());
+  const int unit = static_cast<int>(blockIdx.x) >> 1;
+  const int units = static_cast<int>(gridDim.x) >> 1;
+  const int NT = p.nt, half = NT / 2;
 
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -193,15 +544,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_dfull + 8 * s, 1);
-      mbar_init(bar_dfree + 8 * s, kEpilogue * CG);
+      mbar_init(bar_dfree + 8 * s, 2 * kTcEpilogue);
     }
     mbar_init(bar_fin, 1);
     *abort_flag = 0;
-    *last_flag = 0;
     fence_mbar_init();
   }
   if (warp == kTcMma) {
-    tc_alloc<CG>(slot_tmem, C::TMEM);
+    tc_alloc<2>(slot_tmem, kTmemCols);
     tc_fence_before();
   }
   if (warp == kTcProducer && lane == 0) {
@@ -209,68 +559,45 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     prefetch_tensormap(&wmap);
   }
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync_all();
+  cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base =
       *reinterpret_cast<volatile uint32_t*>(gbase + (slot_tmem - base));
   griddep_wait();
   griddep_launch_dependents();
 
-  const int64_t W = static_cast<int64_t>(p.n_rt) * p.n_tt * p.nkb;
-  const int64_t r0 = range_begin(W, p.P, unit);
-  const int64_t r1 = range_begin(W, p.P, unit + 1);
+  const int tiles = p.n_rt * p.n_tt;
   const uint64_t tmo = p.timeout_ns;
-  const int hrows = p.swiglu ? p.N / 2 : p.N;               // output columns
-  constexpr int SW_ROWS = 64 * CG;                          // outputs of a SwiGLU tile
+  const int cta_rows = p.swiglu ? 64 : kRows;               // output columns of this CTA's rows
 
   if (warp == kTcProducer) {
-    // ------------------------------------------------------------ producer
     if (lane == 0) {
-      const uint32_t full0 = CG == 2 ? cluster_addr(bar_full, 0) : bar_full;
+      const uint32_t full0 = cluster_addr(bar_full, 0);
+      const uint32_t bytes = 2u * static_cast<uint32_t>(C::A_BYTES + half * kTcBlock);
       int st = 0, loads = 0;
       uint32_t round = 0;
       bool ok = true;
-      for (int64_t x = r0; ok && x < r1;) {
-        const Segment sg = segment_at(x, r1, p.nkb);
-        const int tt = sg.t / p.n_rt, rt = sg.t - tt * p.n_rt;
-        const int m0 = tt * NT + static_cast<int>(rank) * C::B_ROWS;
-        const int w0 = p.swiglu ? rt * SW_ROWS + static_cast<int>(rank) * 64
-                                : (rt * CG + static_cast<int>(rank)) * kRows;
-        for (int kb = sg.s0; kb < sg.s1; ++kb) {
+      for (int t = unit; ok && t < tiles; t += units) {
+        const int tt = t / p.n_rt, rt = t - tt * p.n_rt;
+        const int m0 = tt * NT + rank * half;
+        const int w0 = (rt * 2 + rank) * cta_rows;
+        for (int kb = 0; kb < p.nkb; ++kb) {
           if (!wait_phase(bar_empty + 8 * st, (round & 1u) ^ 1u, abort_flag, tmo,
                           SITE_I8_EMPTY)) {
             ok = false;
             break;
           }
-          const uint32_t a = base + st * C::STAGE, b = a + C::A_BYTES;
+          const uint32_t a = base + st * C::STAGE;
           const uint32_t bar = full0 + 8 * st;
-          if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * st, C::STAGE * CG);
-          const int k0 = kb * kTcBlock;
-          if (p.swiglu) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if constexpr (CG == 2)
-                tma_load_3d_pair(a + q * 4096, &wmap, k0, w0 + q * 16, 0, bar);
-              else
-                tma_load_3d(a + q * 4096, &wmap, k0, w0 + q * 16, 0, bar);
-            }
-          } else {
-            if constexpr (CG == 2)
-              tma_load_2d_pair(a, &wmap, k0, w0, bar);
-            else
-              tma_load_2d(a, &wmap, k0, w0, bar);
-          }
-          if constexpr (CG == 2)
-            tma_load_2d_pair(b, &xmap, k0, m0, bar);
-          else
-            tma_load_2d(b, &xmap, k0, m0, bar);
+          if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * st, bytes);
+          i8_load_w<true>(p, a, &wmap, kb * kTcBlock, w0, bar);
+          tma_load_2d_pair(a + C::A_BYTES, &xmap, kb * kTcBlock, m0, bar);
           ++loads;
           if (++st == C::STAGES) {
             st = 0;
             ++round;
           }
         }
-        x = sg.end;
       }
       if (*abort_flag) {
         // the copies in flight must land before the CTA ends: the leader sees
@@ -292,22 +619,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     __syncwarp();
   } else if (warp == kTcMma) {
-    // ------------------------------------------------------------ MMA issue
     if (lane == 0 && rank == 0) {
-      const uint32_t idesc = idesc_s8_s32(kRows * CG, NT);
+      const uint32_t idesc = idesc_s8_s32(2 * kRows, NT);
       int st = 0;
-      uint32_t round = 0, tiles = 0;
+      uint32_t round = 0, done = 0;
       bool ok = true;
-      for (int64_t x = r0; ok && x < r1;) {
-        const Segment sg = segment_at(x, r1, p.nkb);
-        const uint32_t db = tiles & 1u;
-        if (!wait_phase(bar_dfree + 8 * db, ((tiles >> 1) & 1u) ^ 1u, abort_flag, tmo,
+      for (int t = unit; ok && t < tiles; t += units) {
+        const uint32_t db = done & 1u;
+        if (!wait_phase(bar_dfree + 8 * db, ((done >> 1) & 1u) ^ 1u, abort_flag, tmo,
                         SITE_I8_DFREE))
           break;
         tc_fence_after();
-        const uint32_t d = tmem_base + db * NT;
+        const uint32_t d = tmem_base + db * C::NT;
         uint32_t acc = 0;
-        for (int kb = sg.s0; kb < sg.s1; ++kb) {
+        for (int kb = 0; kb < p.nkb; ++kb) {
           if (!wait_phase(bar_full + 8 * st, round & 1u, abort_flag, tmo, SITE_I8_FULL)) {
             ok = false;
             break;
@@ -317,160 +642,60 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const uint64_t dbs = smem_desc_sw128(base + st * C::STAGE + C::A_BYTES);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            mma_ss_i8<CG>(d, da + 2 * kk, dbs + 2 * kk, idesc, acc);   // 32 bytes = 2 units of 16
+            mma_ss_i8<2>(d, da + 2 * kk, dbs + 2 * kk, idesc, acc);        // 32 bytes each
             acc = 1;
           }
-          tc_commit<CG>(bar_empty + 8 * st);
+          tc_commit<2>(bar_empty + 8 * st);
           if (++st == C::STAGES) {
             st = 0;
             ++round;
           }
         }
         if (!ok) break;
-        tc_commit<CG>(bar_dfull + 8 * db);
-        ++tiles;
-        x = sg.end;
+        tc_commit<2>(bar_dfull + 8 * db);
+        ++done;
       }
       // the MMAs in flight read both CTAs' shared memory: wait for them
-      tc_commit<CG>(bar_fin);
+      tc_commit<2>(bar_fin);
       volatile int dummy = 0;
       mbar_wait(bar_fin, 0, &dummy, tmo, SITE_TEARDOWN);
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ epilogue
-    const int i = tid;                                      // TMEM lane
-    const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t dfree0 = CG == 2 ? cluster_addr(bar_dfree, 0) : bar_dfree;
-    const int first_tile = static_cast<int>(r0 / p.nkb);
-    const int cta = unit * CG + static_cast<int>(rank);
-    uint32_t tiles = 0;
-    for (int64_t x = r0; x < r1;) {
-      const Segment sg = segment_at(x, r1, p.nkb);
-      const int tt = sg.t / p.n_rt, rt = sg.t - tt * p.n_rt;
-      const int m0 = tt * NT;
-      const int mv = p.M - m0 < NT ? p.M - m0 : NT;
-      const int chunks = (mv + 15) >> 4;
-      // this lane's weight row, and the output column it stores
-      int wrow, col;
-      if (p.swiglu) {
-        col = rt * SW_ROWS + static_cast<int>(rank) * 64 + warp * 16 + (lane & 15);
-        wrow = lane < 16 ? col : hrows + col;
-      } else {
-        col = wrow = (rt * CG + static_cast<int>(rank)) * kRows + i;
-      }
-      const bool live = col < hrows;
-      const float ws = live ? __ldg(p.wscale + wrow) : 0.f;
-      for (int c = i; c < NT; c += kEpilogue)
-        s_sx[c] = c < mv ? __fdiv_rn(__ldg(p.absmax + m0 + c), 127.0f) : 0.f;
-      const uint32_t db = tiles & 1u;
-      const bool ok = wait_phase(bar_dfull + 8 * db, (tiles >> 1) & 1u, abort_flag, tmo,
+    const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t dfree0 = cluster_addr(bar_dfree, 0);
+    uint32_t done = 0;
+    for (int t = unit; t < tiles; t += units) {
+      const int tt = t / p.n_rt, rt = t - tt * p.n_rt;
+      const I8Lane l = i8_lane(p, (rt * 2 + rank) * cta_rows, tt * NT, NT);
+      i8_load_scales(p, l.m0, l.mv, NT, s_sx);
+      const uint32_t db = done & 1u;
+      const bool ok = wait_phase(bar_dfull + 8 * db, (done >> 1) & 1u, abort_flag, tmo,
                                  SITE_I8_DFULL);
-      if (!vote_all_epilogue(ok)) break;                    // also orders s_sx
+      if (!tc_epilogue_vote(ok)) break;                     // also orders s_sx
       tc_fence_after();
-      const uint32_t daddr = tmem_base + lane_addr + db * NT;
-      // scale, SwiGLU and store 16 columns
-      auto finish = [&](const int (&a)[16], int c0) {
-        float v[16];
-#pragma unroll
-        for (int q = 0; q < 16; ++q)
-          v[q] = __fmul_rn(__fmul_rn(s_sx[c0 + q], ws), static_cast<float>(a[q]));
-        if (p.swiglu) {
-          // lanes 0-15 hold gate and lanes 16-31 up of the same outputs; of two
-          // columns the lower half takes the first and the upper half the second
-          const bool hi = lane >= 16;
-#pragma unroll
-          for (int q = 0; q < 16; q += 2) {
-            const float other = __shfl_xor_sync(0xffffffffu, hi ? v[q] : v[q + 1], 16);
-            const float h = hi ? i8_swiglu_f32(other, v[q + 1]) : i8_swiglu_f32(v[q], other);
-            const int m = c0 + q + (hi ? 1 : 0);
-            if (live && m < mv) {
-              const int64_t o = static_cast<int64_t>(m0 + m) * hrows + col;
-              if (p.out_bf16)
-                static_cast<uint16_t*>(p.y)[o] = bf16_bits(h);
-              else
-                static_cast<float*>(p.y)[o] = h;
-            }
-          }
-        } else if (live) {
-          const int64_t o = static_cast<int64_t>(m0 + c0) * hrows + col;
-#pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            if (c0 + q >= mv) break;
-            if (p.out_bf16)
-              static_cast<uint16_t*>(p.y)[o + static_cast<int64_t>(q) * hrows] = bf16_bits(v[q]);
-            else
-              static_cast<float*>(p.y)[o + static_cast<int64_t>(q) * hrows] = v[q];
-          }
-        }
-      };
-      const bool whole = sg.s0 == 0 && sg.s1 == p.nkb;
-      const int slot = 2 * cta + (sg.t == first_tile ? 0 : 1);
-      int* const mine = p.partial + static_cast<int64_t>(slot) * NT * kRows;
-      for (int cc = 0; cc < chunks; ++cc) {
+      const uint32_t daddr = tmem_base + lane_addr + db * C::NT;
+      for (int cc = l.half; cc * 16 < l.mv; cc += 2) {
         uint32_t r[16];
         tmem_ld16(daddr + cc * 16, r);
         tmem_wait_ld();
         int a[16];
 #pragma unroll
         for (int q = 0; q < 16; ++q) a[q] = static_cast<int>(r[q]);
-        if (whole) {
-          finish(a, cc * 16);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 16; ++q)
-            if (cc * 16 + q < mv) __stcg(mine + (cc * 16 + q) * kRows + i, a[q]);
-        }
+        i8_finish<16>(p, l, s_sx, a, cc * 16);
       }
       tc_fence_before();
-      if constexpr (CG == 2)
-        mbar_arrive_cluster(dfree0 + 8 * db);
-      else
-        mbar_arrive(dfree0 + 8 * db);
-      ++tiles;
-      if (!whole) {
-        __threadfence();
-        named_bar_epilogue();
-        const int64_t t0 = static_cast<int64_t>(sg.t) * p.nkb;
-        const int c_lo = owner_of(W, p.P, t0), c_hi = owner_of(W, p.P, t0 + p.nkb - 1);
-        // a unit is the first owner of at most one cut tile: its counter
-        int* const cnt = p.counter + c_lo * CG + rank;
-        if (i == 0) {
-          const int old = atomicAdd(cnt, 1);
-          *last_flag = old == c_hi - c_lo;
-          if (old == c_hi - c_lo) *cnt = 0;
-        }
-        named_bar_epilogue();
-        if (*last_flag) {
-          __threadfence();
-          for (int cc = 0; cc < chunks; ++cc) {
-            int a[16];
-#pragma unroll
-            for (int q = 0; q < 16; ++q) a[q] = 0;
-            for (int c = c_lo; c <= c_hi; ++c) {
-              const int ft = static_cast<int>(range_begin(W, p.P, c) / p.nkb);
-              const int sl = 2 * (c * CG + static_cast<int>(rank)) + (sg.t == ft ? 0 : 1);
-              const int* src = p.partial + static_cast<int64_t>(sl) * NT * kRows;
-#pragma unroll
-              for (int q = 0; q < 16; ++q)
-                if (cc * 16 + q < mv) a[q] += __ldcg(src + (cc * 16 + q) * kRows + i);
-            }
-            finish(a, cc * 16);
-          }
-        }
-        named_bar_epilogue();
-      } else {
-        named_bar_epilogue();                               // s_sx is rewritten next
-      }
-      x = sg.end;
+      mbar_arrive_cluster(dfree0 + 8 * db);
+      ++done;
+      tc_epilogue_vote(true);                               // s_sx is rewritten next
     }
   }
 
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync_all();
+  cluster_sync_all();
   if (warp == kTcMma) {
     tc_fence_after();
-    tc_dealloc<CG>(tmem_base, C::TMEM);
+    tc_dealloc<2>(tmem_base, kTmemCols);
   }
 }
 

@@ -325,9 +325,9 @@ CQ_API int cq_moe_grouped_gemm(const uint16_t *tokens, int64_t T, const int32_t 
  *   epilogue CQ_EPI_NONE: y [M][N]; CQ_EPI_SWIGLU: rows [0,N/2) of W are
  *            gate, the others up, y is [M][N/2]; requires N even
  *   y        float or bfloat16 (out_dtype)
- *   workspace  device scratch of cq_gemm_i8_workspace_size(...) bytes, 256-byte
- *            aligned (may be NULL when that size is 0), zero before the first
- *            call that uses it; every completed call leaves its counters zero
+ *   workspace  device scratch of cq_gemm_i8_workspace_size(...) bytes for the
+ *            rows cq_linear_i8 quantizes, 256-byte aligned (may be NULL when
+ *            that size is 0; cq_gemm_i8 takes the same arguments and needs none)
  * K a multiple of 16, at most 131072; M, N at most 2^24; x, wq, y 16-byte
  * aligned.  |acc| <= 2^31 is exact: 127^2 * 131072 = 2,114,060,288.  A value
  * of -128 in wq or xq counts as such (and the bound then needs K < 131072).
