@@ -44,9 +44,12 @@ extern "C" CQ_API int cq_moe_route(const void* logits, int logits_dtype, int64_t
   p.renorm = renorm;
   p.bf16 = logits_dtype == CQ_DTYPE_BF16;
   p.scale = scale;
+  p.vec4 = E % 4 == 0 && aligned(logits, p.bf16 ? 8 : 16) && (!bias || aligned(bias, 16));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // registers for the row's logits: 32 per unit of NV
+  // NV values in each of 32 lanes (a multiple of 4: whole vectors)
   if (E <= 128) return launch_route<4>(p, s);
+  if (E <= 256) return launch_route<8>(p, s);
   if (E <= 512) return launch_route<16>(p, s);
+  if (E <= 896) return launch_route<28>(p, s);
   return launch_route<32>(p, s);
 }

@@ -33,13 +33,13 @@ struct RouteParams {
   float* w;                 // [T][k]
   int64_t T;
   int E, k;
-  int sigmoid, renorm, bf16;
+  int sigmoid, renorm, bf16, vec4;
   float scale;
 };
 
 struct RouteSmem {
   double pick[kRtCand];
-  float logit[kRtCand];
+  double score[kRtCand];
   int id[kRtCand];
   double sel_score[kRtMaxTopk];
   int sel_id[kRtMaxTopk];
@@ -56,6 +56,44 @@ __device__ __forceinline__ double route_exp64(float l, float top) {
   return l == top ? 1.0 : exp(static_cast<double>(l) - static_cast<double>(top));
 }
 
+// One logit, NaN as -inf.
+__device__ __forceinline__ float route_logit(const RouteParams& p, int64_t at) {
+  const float v = p.bf16 ? __uint_as_float(static_cast<uint32_t>(__ldg(
+                               static_cast<const uint16_t*>(p.logits) + at)) << 16)
+                         : __ldg(static_cast<const float*>(p.logits) + at);
+  return fmaxf(v, -INFINITY);
+}
+
+// 2^x and 1/x by the approximate units (2 and 1 units in the last place;
+// 2^x of +inf is inf, 1/inf is 0).
+__device__ __forceinline__ float route_ex2(float x) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float route_rcp(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// The warp's values in descending order, one per lane.
+__device__ __forceinline__ float warp_sort_desc(float v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2) {
+#pragma unroll
+    for (int o = size / 2; o > 0; o /= 2) {
+      const float u = __shfl_xor_sync(0xffffffffu, v, o);
+      const bool first = (lane & o) == 0, down = (lane & size) == 0;
+      v = first == down ? fmaxf(v, u) : fminf(v, u);
+    }
+  }
+  return v;
+}
+
+// NV values per lane.  The lane's value i is expert ((i / 4) 32 + lane) 4 + i % 4
+// where rows and bias can be read in fours (vec4), else i 32 + lane.
 template <int NV>
 __global__ void __launch_bounds__(kRtWarps * 32)
     route_topk_kernel(const __grid_constant__ RouteParams p) {
@@ -67,36 +105,63 @@ __global__ void __launch_bounds__(kRtWarps * 32)
   griddep_launch_dependents();
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRtWarps + warp;
   if (t >= p.T) return;
-  float l[NV], key[NV];
   const int64_t base = t * p.E;
+  auto expert = [&](int i) {
+    return p.vec4 ? ((i >> 2) * 32 + lane) * 4 + (i & 3) : i * 32 + lane;
+  };
+  float key[NV];                         // the logits, then the FP32 picks
+  if (p.vec4) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = i * 32 + lane;
-    float v = NEG;
-    if (e < p.E)
-      v = p.bf16 ? __uint_as_float(static_cast<uint32_t>(
-                       __ldg(static_cast<const uint16_t*>(p.logits) + base + e)) << 16)
-                 : __ldg(static_cast<const float*>(p.logits) + base + e);
-    l[i] = v == v ? v : NEG;
+    for (int i = 0; i < NV; i += 4) {
+      const int e = expert(i);
+      float4 v = make_float4(NEG, NEG, NEG, NEG);
+      if (e < p.E) {
+        if (p.bf16) {
+          const uint2 q =
+              __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.logits) + base +
+                                                   e));
+          v = make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xFFFF0000u),
+                          __uint_as_float(q.y << 16), __uint_as_float(q.y & 0xFFFF0000u));
+        } else {
+          v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.logits) + base +
+                                                    e));
+        }
+      }
+      key[i] = v.x;
+      key[i + 1] = v.y;
+      key[i + 2] = v.z;
+      key[i + 3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) key[i] = fmaxf(key[i], NEG);      // NaN becomes -inf
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = i * 32 + lane;
+      key[i] = e < p.E ? route_logit(p, base + e) : NEG;
+    }
   }
   float top = NEG;
   double sum = 0.0;                      // softmax: sum of exp(l - top)
   if (!p.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) top = fmaxf(top, l[i]);
+    for (int i = 0; i < NV; ++i) top = fmaxf(top, key[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (p.bias) {
-      // picks compare p + bias: the sum in FP64
+      // picks compare p + bias: the sum in FP64 (the logits read again, so
+      // that the loop stays rolled)
 #pragma unroll 1
-      for (int i = 0; i < NV; ++i)
-        if (l[i] > NEG) sum += route_exp64(l[i], top);
+      for (int e = lane; e < p.E; e += 32) {
+        const float v = route_logit(p, base + e);
+        if (v > NEG) sum += route_exp64(v, top);
+      }
       sum = warp_sum_f64(sum);
     } else if (!p.renorm) {
       float f = 0.f;                     // only scales the weights: FP32
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (l[i] > NEG) f += l[i] == top ? 1.f : expf(l[i] - top);
+        if (key[i] > NEG) f += key[i] == top ? 1.f : expf(key[i] - top);
       sum = warp_sum_f64(static_cast<double>(f));
     }
   }
@@ -104,89 +169,107 @@ __global__ void __launch_bounds__(kRtWarps * 32)
     if (p.sigmoid) return 1.0 / (1.0 + exp(-static_cast<double>(v)));
     return p.bias ? route_exp64(v, top) / sum : route_exp64(v, top);
   };
-  auto pick64 = [&](float v, int e) -> double {
-    return p.bias ? score64(v) + static_cast<double>(__ldg(p.bias + e))
-                  : static_cast<double>(v);
-  };
-  // FP32 picks (clamped, so that the margin below stays finite)
-  const float inv_sum = static_cast<float>(1.0 / sum);
+  if (p.bias) {
+    // FP32 picks
+    constexpr float LOG2E = 1.44269504f;
+    const float inv_sum = p.sigmoid ? 0.f : static_cast<float>(1.0 / sum);
+#pragma unroll
+    for (int i = 0; i < NV; i += 4) {
+      float b[4];
+      if (p.vec4) {
+        const int e = expert(i);
+        const float4 q = e < p.E ? __ldg(reinterpret_cast<const float4*>(p.bias + e))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+        b[0] = q.x;
+        b[1] = q.y;
+        b[2] = q.z;
+        b[3] = q.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int e = expert(i + j);
+          b[j] = e < p.E ? __ldg(p.bias + e) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float v = key[i + j];
+        const float sc = p.sigmoid ? route_rcp(1.0f + route_ex2(-LOG2E * v))
+                                   : (v == top ? 1.0f : route_ex2(LOG2E * (v - top))) * inv_sum;
+        key[i + j] = v > NEG ? fmaxf(sc + b[j], NEG) : NEG;
+      }
+    }
+  }
   float best = NEG;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = i * 32 + lane;
-    float v = l[i];
-    if (p.bias && v > NEG) {
-      const float sc = p.sigmoid ? 1.0f / (1.0f + expf(-v))
-                                 : (v == top ? 1.f : expf(v - top)) * inv_sum;
-      v = sc + __ldg(p.bias + e);
-      v = v == v ? fminf(v, 3e38f) : NEG;
-    }
-    key[i] = v;
-    best = fmaxf(best, v);
+  for (int i = 0; i < NV; ++i) best = fmaxf(best, key[i]);
+  // the k-th largest lane maximum, and its margin.  An FP32 pick is off by at
+  // most 5e-7 (1 + |bias|): the score is at most 1, its exponential within
+  // 2^-21 + 2^-22 |l| (relative, and s (1 - s) |l| < 0.23), the reciprocal and
+  // the sums within a few 2^-24.  Twice that on either side, with
+  // |bias| <= 1 + |pick|.
+  float cut = __shfl_sync(0xffffffffu, warp_sort_desc(best), p.k - 1);
+  if (p.bias) {
+    cut = fminf(cut, 3e38f);
+    cut -= 2e-6f * (2.0f + fabsf(cut));
   }
-  // the k-th largest lane maximum
-  int rank = 0;
+  cut = fmaxf(cut, -3.402823466e38f);        // -inf is never a candidate
+  uint32_t mask = 0;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const float o = __shfl_sync(0xffffffffu, best, j);
-    rank += o > best || (o == best && j < lane);
-  }
-  const unsigned at = __ballot_sync(0xffffffffu, rank == p.k - 1);
-  float cut = __shfl_sync(0xffffffffu, best, __ffs(at) - 1);
-  // FP32 picks are off by a few units of 2^-24 (1 + |bias|), the score being
-  // at most 1: twice that on either side, rounded up
-  if (p.bias && cut > NEG) cut -= 2e-6f * (2.0f + fabsf(cut));
-  int n = 0;
+  for (int i = 0; i < NV; ++i) mask |= key[i] >= cut ? 1u << i : 0u;
+  const int mine = __popc(mask);
+  int n = mine;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const bool in = key[i] > NEG && key[i] >= cut;
-    const unsigned m = __ballot_sync(0xffffffffu, in);
-    const int pos = n + __popc(m & ((1u << lane) - 1u));
-    if (in && pos < kRtCand) {
-      s.id[pos] = i * 32 + lane;
-      s.logit[pos] = l[i];
-    }
-    n += __popc(m);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, n, o);
+    if (lane >= o) n += u;
   }
+  int pos = n - mine;
+  n = __shfl_sync(0xffffffffu, n, 31);
   if (lane < p.k) s.sel_id[lane] = -1;
-  __syncwarp();
   if (n <= kRtCand) {
-    for (int c = lane; c < n; c += 32) s.pick[c] = pick64(s.logit[c], s.id[c]);
+    for (uint32_t m = mask; m; m &= m - 1) s.id[pos++] = expert(__ffs(m) - 1);
     __syncwarp();
-    // candidates are in the order of their ids, so position breaks ties
     for (int c = lane; c < n; c += 32) {
-      const double mine = s.pick[c];
+      const int e = s.id[c];
+      const float v = route_logit(p, base + e);
+      const double sc = score64(v);
+      s.score[c] = sc;
+      s.pick[c] = p.bias ? sc + static_cast<double>(__ldg(p.bias + e)) : static_cast<double>(v);
+    }
+    __syncwarp();
+    for (int c = lane; c < n; c += 32) {
+      const double pick = s.pick[c];
+      const int e = s.id[c];
       int r = 0;
       for (int j = 0; j < n; ++j) {
         const double o = s.pick[j];
-        r += o > mine || (o == mine && j < c);
+        r += o > pick || (o == pick && s.id[j] < e);
       }
-      if (r < p.k && mine > -static_cast<double>(INFINITY)) {
-        s.sel_id[r] = s.id[c];
-        s.sel_score[r] = score64(s.logit[c]);
+      if (r < p.k && pick > -static_cast<double>(INFINITY)) {
+        s.sel_id[r] = e;
+        s.sel_score[r] = s.score[c];
       }
     }
   } else {
     // more equal (or nearly equal) picks than are ranked at once: take the
     // best k one by one
-    uint32_t taken = 0;
+    __syncwarp();
     for (int r = 0; r < p.k; ++r) {
-      double bp = -static_cast<double>(INFINITY);
-      int be = kRtMaxExperts, bi = -1;
-      float bl = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (!(key[i] > NEG && key[i] >= cut) || (taken >> i & 1u)) continue;
-        const double v = pick64(l[i], i * 32 + lane);
-        if (v > bp) {
-          bp = v;
-          be = i * 32 + lane;
-          bi = i;
-          bl = l[i];
+      double wp = -static_cast<double>(INFINITY);
+      int we = kRtMaxExperts, wi = 0;
+      for (uint32_t m = mask; m; m &= m - 1) {
+        const int i = __ffs(m) - 1, e = expert(i);
+        const float v = route_logit(p, base + e);
+        const double pick = p.bias ? score64(v) + static_cast<double>(__ldg(p.bias + e))
+                                   : static_cast<double>(v);
+        if (pick > wp || (pick == wp && e < we)) {
+          wp = pick;
+          we = e;
+          wi = i;
         }
       }
-      double wp = bp;
-      int we = be;
+      const int own = we;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         const double op = __shfl_xor_sync(0xffffffffu, wp, o);
@@ -196,10 +279,10 @@ __global__ void __launch_bounds__(kRtWarps * 32)
           we = oe;
         }
       }
-      if (we == be && bi >= 0) {
-        taken |= 1u << bi;
-        s.sel_id[r] = be;
-        s.sel_score[r] = score64(bl);
+      if (we == own && we < kRtMaxExperts && wp > -static_cast<double>(INFINITY)) {
+        mask &= ~(1u << wi);
+        s.sel_id[r] = we;
+        s.sel_score[r] = score64(route_logit(p, base + we));
       }
     }
   }
