@@ -34,6 +34,7 @@ constexpr int kI8MaxTokens = 16;             // tokens of one pass
 constexpr int kI8MaxRoutes = 1024;           // routes of one launch of the MoE layer
 constexpr int kI8MaxExperts = 16384;
 constexpr int kI8CombineRows = 32;           // output columns of one combine block
+constexpr int kI8DoneWords = 16;              // 512 output blocks of a pass, at most
 constexpr int kI8SmemLimit = 227 * 1024;
 
 // Bytes between two activation rows in shared memory: whole steps, plus 64 so
@@ -160,117 +161,132 @@ struct I8Pass {
   int nr;
 };
 
-// acc[tile][16][cnt] += the products of the pass's rows with the `cnt` staged
-// activation rows.  acc is zero on entry; a barrier follows before it is read.
+// The multiplication of one pass.  begin() issues the warp's first loads, so
+// that they are in flight while the CTA stages activations or finishes the
+// pass before; run() adds the products of the pass's rows with the `cnt`
+// staged activation rows to acc[tile][16][cnt] (zero on entry, complete after
+// a barrier).
 template <int NB>
-__device__ __forceinline__ void i8_stream(const I8Pass& ps, int cnt, int K, const int8_t* xs,
-                                          int stride, int* acc) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const bool paired = ps.wb != nullptr;
-  const int rpt = paired ? 8 : 16;
-  const int tiles = (ps.nr + rpt - 1) / rpt;
-  const int nk = (K + kI8Step - 1) / kI8Step;
-  const int total = tiles * nk;
-  const int b0 = static_cast<int>(static_cast<int64_t>(warp) * total / kI8Warps);
-  const int b1 = static_cast<int>(static_cast<int64_t>(warp + 1) * total / kI8Warps);
-  if (b0 >= b1) return;
-  int tile = b0 / nk, kb = b0 - tile * nk;
+struct I8Stream {
+  const int8_t *wa, *wb;    // wb == null: not paired
+  int nr, K, nk;
+  int steps;                // 256-byte steps of this warp
+  int tile, kb;             // the next step to multiply
+  int lt, lk;               // the step loaded last
+  const int8_t *pa, *pb;    // this lane's two rows of tile lt, null past the last row
+  uint4 a0[4], w0[4];
 
-  // the pointers of this lane's two rows in a tile, null past the last row
-  const int8_t *pa = nullptr, *pb = nullptr;
-  auto set_tile = [&](int tl) {
-    const int ra = tl * rpt + g;
-    const int rb = paired ? ra : ra + 8;
-    const int8_t* base_b = paired ? ps.wb : ps.wa;
-    pa = ra < ps.nr ? ps.wa + static_cast<int64_t>(ra) * K + t * 16 : nullptr;
-    pb = rb < ps.nr ? base_b + static_cast<int64_t>(rb) * K + t * 16 : nullptr;
-  };
-  auto load = [&](int kk, uint4 (&a)[4], uint4 (&b)[4]) {
+  __device__ __forceinline__ void set_tile() {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int ra = lt * (wb ? 8 : 16) + g;
+    const int rb = wb ? ra : ra + 8;
+    const int8_t* base_b = wb ? wb : wa;
+    pa = ra < nr ? wa + static_cast<int64_t>(ra) * K + t * 16 : nullptr;
+    pb = rb < nr ? base_b + static_cast<int64_t>(rb) * K + t * 16 : nullptr;
+  }
+  __device__ __forceinline__ void load(uint4 (&a)[4], uint4 (&b)[4]) const {
+    const int t = threadIdx.x & 3;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const int k = kk * kI8Step + s * 64;
+      const int k = lk * kI8Step + s * 64;
       const bool in = k + t * 16 < K;
       a[s] = in && pa ? ldg_stream16(pa + k) : make_uint4(0, 0, 0, 0);
       b[s] = in && pb ? ldg_stream16(pb + k) : make_uint4(0, 0, 0, 0);
     }
-  };
-  int d[NB][4];
-#pragma unroll
-  for (int n = 0; n < NB; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) d[n][i] = 0;
-  auto flush = [&](int tl) {
-    int* at = acc + tl * 16 * cnt;
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int col = n * 8 + 2 * t + (i & 1);
-        if (col < cnt) atomicAdd(at + (g + 8 * (i >> 1)) * cnt + col, d[n][i]);
-        d[n][i] = 0;
-      }
-    }
-  };
-  const bool has0 = g < cnt, has1 = NB > 1 && g + 8 < cnt;
-  const int8_t* x0 = xs + g * stride + t * 16;
-  const int8_t* x1 = xs + (g + 8) * stride + t * 16;
-  auto compute = [&](int kk, const uint4 (&a)[4], const uint4 (&b)[4]) {
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int k = kk * kI8Step + s * 64;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (has0) x = *reinterpret_cast<const uint4*>(x0 + k);
-      mma_16832_s8(d[0], a[s].x, b[s].x, a[s].y, b[s].y, x.x, x.y);
-      mma_16832_s8(d[0], a[s].z, b[s].z, a[s].w, b[s].w, x.z, x.w);
-      if constexpr (NB > 1) {
-        if (cnt > 8) {
-          uint4 z = make_uint4(0, 0, 0, 0);
-          if (has1) z = *reinterpret_cast<const uint4*>(x1 + k);
-          mma_16832_s8(d[1], a[s].x, b[s].x, a[s].y, b[s].y, z.x, z.y);
-          mma_16832_s8(d[1], a[s].z, b[s].z, a[s].w, b[s].w, z.z, z.w);
-        }
-      }
-    }
-  };
-  // two register buffers: the next step's loads are in flight while this one
-  // is multiplied
-  uint4 a0[4], w0[4], a1[4], w1[4];
-  set_tile(tile);
-  load(kb, a0, w0);
-  int lt = tile, lk = kb;                       // the step loaded last
-  auto advance = [&]() {
+  }
+  __device__ __forceinline__ void advance() {
     if (++lk == nk) {
       lk = 0;
-      set_tile(++lt);
-    }
-  };
-  auto done = [&]() {                           // after computing step (tile, kb)
-    if (++kb == nk) {
-      flush(tile);
-      kb = 0;
-      ++tile;
-    }
-  };
-  for (int b = b0; b < b1; b += 2) {
-    const bool two = b + 1 < b1;
-    if (two) {
-      advance();
-      load(lk, a1, w1);
-    }
-    compute(kb, a0, w0);
-    done();
-    if (b + 2 < b1) {
-      advance();
-      load(lk, a0, w0);
-    }
-    if (two) {
-      compute(kb, a1, w1);
-      done();
+      ++lt;
+      set_tile();
     }
   }
-  if (kb != 0) flush(tile);
-}
+
+  __device__ __forceinline__ void begin(const I8Pass& ps, int K_) {
+    const int warp = threadIdx.x >> 5;
+    wa = ps.wa;
+    wb = ps.wb;
+    nr = ps.nr;
+    K = K_;
+    nk = (K + kI8Step - 1) / kI8Step;
+    const int rpt = wb ? 8 : 16;
+    const int total = (nr + rpt - 1) / rpt * nk;
+    const int b0 = static_cast<int>(static_cast<int64_t>(warp) * total / kI8Warps);
+    const int b1 = static_cast<int>(static_cast<int64_t>(warp + 1) * total / kI8Warps);
+    steps = b1 - b0;
+    if (steps == 0) return;
+    lt = tile = b0 / nk;
+    lk = kb = b0 - tile * nk;
+    set_tile();
+    load(a0, w0);
+  }
+
+  __device__ __forceinline__ void run(int cnt, const int8_t* xs, int stride, int* acc) {
+    if (steps == 0) return;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    int d[NB][4];
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[n][i] = 0;
+    auto flush = [&]() {
+      int* at = acc + tile * 16 * cnt;
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int col = n * 8 + 2 * t + (i & 1);
+          if (col < cnt) atomicAdd(at + (g + 8 * (i >> 1)) * cnt + col, d[n][i]);
+          d[n][i] = 0;
+        }
+      }
+    };
+    const bool has0 = g < cnt, has1 = NB > 1 && g + 8 < cnt;
+    const int8_t* x0 = xs + g * stride + t * 16;
+    const int8_t* x1 = xs + (g + 8) * stride + t * 16;
+    // multiply the step (tile, kb) and move on
+    auto compute = [&](const uint4 (&a)[4], const uint4 (&b)[4]) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int k = kb * kI8Step + s * 64;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (has0) x = *reinterpret_cast<const uint4*>(x0 + k);
+        mma_16832_s8(d[0], a[s].x, b[s].x, a[s].y, b[s].y, x.x, x.y);
+        mma_16832_s8(d[0], a[s].z, b[s].z, a[s].w, b[s].w, x.z, x.w);
+        if constexpr (NB > 1) {
+          if (cnt > 8) {
+            uint4 z = make_uint4(0, 0, 0, 0);
+            if (has1) z = *reinterpret_cast<const uint4*>(x1 + k);
+            mma_16832_s8(d[1], a[s].x, b[s].x, a[s].y, b[s].y, z.x, z.y);
+            mma_16832_s8(d[1], a[s].z, b[s].z, a[s].w, b[s].w, z.z, z.w);
+          }
+        }
+      }
+      if (++kb == nk) {
+        flush();
+        kb = 0;
+        ++tile;
+      }
+    };
+    // two register buffers: the next step's loads are in flight while this
+    // one is multiplied
+    uint4 a1[4], w1[4];
+    for (int b = 0; b < steps; b += 2) {
+      const bool two = b + 1 < steps;
+      if (two) {
+        advance();
+        load(a1, w1);
+      }
+      compute(a0, w0);
+      if (b + 2 < steps) {
+        advance();
+        load(a0, w0);
+      }
+      if (two) compute(a1, w1);
+    }
+    if (kb != 0) flush();
+  }
+};
 
 // silu(g) * u with silu(g) = g / (1 + exp(-g)), in FP32.
 __device__ __forceinline__ float i8_swiglu_f32(float g, float u) {
@@ -307,26 +323,37 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   griddep_wait();
   griddep_launch_dependents();
   if (r0 >= r1) return;
+  const int rpt = p.swiglu ? 8 : 16;
+  const int per_pass = kI8AccBytes / (64 * p.M) * rpt;      // rows whose accumulators fit
+  auto pass_at = [&](int a) {
+    I8Pass ps;
+    ps.nr = r1 - a < per_pass ? r1 - a : per_pass;
+    ps.wa = p.w + static_cast<int64_t>(a) * p.K;
+    ps.wb = p.swiglu ? ps.wa + static_cast<int64_t>(rows) * p.K : nullptr;
+    return ps;
+  };
+  I8Pass ps = pass_at(r0);
+  I8Stream<NB> stream;
+  stream.begin(ps, p.K);
   I8Rows src;
   src.base = p.x;
   src.absmax = p.absmax;
   src.rows = nullptr;
   src.div = 1;
   i8_stage_rows<SRC>(src, p.M, p.K, xs, p.stride, s_max, s_scale);
-  const int rpt = p.swiglu ? 8 : 16;
-  const int per_pass = kI8AccBytes / (64 * p.M) * rpt;      // rows whose accumulators fit
-  for (int a = r0; a < r1; a += per_pass) {
-    I8Pass ps;
-    ps.nr = r1 - a < per_pass ? r1 - a : per_pass;
-    ps.wa = p.w + static_cast<int64_t>(a) * p.K;
-    ps.wb = p.swiglu ? ps.wa + static_cast<int64_t>(rows) * p.K : nullptr;
+  for (int a = r0; a < r1;) {
     const int tiles = (ps.nr + rpt - 1) / rpt;
     for (int i = tid; i < tiles * 16 * p.M; i += kI8Threads) acc[i] = 0;
     __syncthreads();
-    i8_stream<NB>(ps, p.M, p.K, xs, p.stride, acc);
+    stream.run(p.M, xs, p.stride, acc);
+    const int nr = ps.nr;
+    if (a + nr < r1) {
+      ps = pass_at(a + nr);
+      stream.begin(ps, p.K);
+    }
     __syncthreads();
-    for (int i = tid; i < ps.nr * p.M; i += kI8Threads) {
-      const int m = i / ps.nr, r = i - m * ps.nr;
+    for (int i = tid; i < nr * p.M; i += kI8Threads) {
+      const int m = i / nr, r = i - m * nr;
       const int at = (p.swiglu ? (r >> 3) * 16 + (r & 7) : r) * p.M + m;
       const float sx = s_scale[m];
       float v = __fmul_rn(__fmul_rn(sx, p.wscale[a + r]), static_cast<float>(acc[at]));
@@ -342,6 +369,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         static_cast<float*>(p.y)[o] = v;
     }
     __syncthreads();
+    a += nr;
   }
 }
 
@@ -426,7 +454,53 @@ __device__ __forceinline__ void i8_prefix(int n, int* out, int* part, F value) {
   __syncthreads();
 }
 
+// The plan of at most 32 routes, by the first warp (experts in the order of
+// their first route; the order only decides which CTA works on what).
+__device__ __forceinline__ void i8_plan_small(const I8MoeParams& p, I8PlanSmem& s) {
+  const int lane = threadIdx.x;
+  if (lane < 32) {
+    int id = lane < p.R ? __ldg(p.ids + lane) : -1;
+    if (id < 0 || id >= p.E) id = -1;
+    const unsigned same = __match_any_sync(0xffffffffu, id);
+    const unsigned below = (1u << lane) - 1u;
+    const bool first = id >= 0 && (same & below) == 0;
+    const unsigned firsts = __ballot_sync(0xffffffffu, first);
+    const int cnt = first ? __popc(same) : 0, chunks = (cnt + p.nt - 1) / p.nt;
+    int off = cnt, ch = chunks;                  // inclusive prefixes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, off, o), v = __shfl_up_sync(0xffffffffu, ch, o);
+      if (lane >= o) {
+        off += u;
+        ch += v;
+      }
+    }
+    const int leader = __ffs(same) - 1;
+    const int base = __shfl_sync(0xffffffffu, off - cnt, leader);
+    const int d = __popc(firsts & ((1u << leader) - 1u));
+    if (first) {
+      s.expert[d] = id;
+      s.off[d] = off - cnt;
+      s.chunk[d] = ch - chunks;
+    }
+    s.dense[lane] = static_cast<int16_t>(id >= 0 ? d : -1);
+    if (id >= 0) s.route[base + __popc(same & below)] = lane;
+    if (lane == 31) {
+      const int ne = __popc(firsts);
+      s.n_experts = ne;
+      s.n_chunks = ch;
+      s.off[ne] = off;
+      s.chunk[ne] = ch;
+    }
+  }
+  __syncthreads();
+}
+
 __device__ __forceinline__ void i8_plan(const I8MoeParams& p, I8PlanSmem& s) {
+  if (p.R <= 32) {
+    i8_plan_small(p, s);
+    return;
+  }
   const int tid = threadIdx.x;
   const int words = (p.E + 31) / 32;
   constexpr int PER = kI8MaxRoutes / kI8Threads;
@@ -488,7 +562,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   __shared__ I8PlanSmem s;
   __shared__ uint32_t s_max[kI8MaxTokens];
   __shared__ float s_scale[kI8MaxTokens];
-  __shared__ int s_last;
+  __shared__ uint32_t s_done[kI8DoneWords];      // output blocks this pass completed
   int8_t* const xs = reinterpret_cast<int8_t*>(i8_smem);
   int* const acc = reinterpret_cast<int*>(i8_smem + p.acc_off);
   const int tid = threadIdx.x;
@@ -503,14 +577,65 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   // the second launch may start before the first has ended: the ids are the
   // caller's and were complete before the first began
   i8_plan(p, s);
-  if constexpr (DOWN) griddep_wait();
   const int nc = s.n_chunks;
+  const int64_t W = static_cast<int64_t>(nc) * rows;
+  int64_t lo = W * blockIdx.x / gridDim.x;       // next row of the chunks' rows
+  const int64_t hi = W * (blockIdx.x + 1) / gridDim.x;
+
+  // the passes of this CTA: rows [a, a + nr) of a chunk, all with its routes
+  struct Work {
+    int ch, first, cnt, a, nr;
+    int64_t e;
+  };
+  auto next = [&](Work& w) {
+    const int ch = static_cast<int>(lo / rows);
+    if (ch != w.ch) {
+      // the chunk's expert: largest d with chunk[d] <= ch
+      int d0 = 0, d1 = s.n_experts;
+      while (d1 - d0 > 1) {
+        const int mid = (d0 + d1) >> 1;
+        if (s.chunk[mid] <= ch) d0 = mid; else d1 = mid;
+      }
+      w.ch = ch;
+      w.first = s.off[d0] + (ch - s.chunk[d0]) * p.nt;
+      const int left = s.off[d0 + 1] - w.first;
+      w.cnt = left < p.nt ? left : p.nt;
+      w.e = s.expert[d0];
+    }
+    const int per_pass = kI8AccBytes / (64 * w.cnt) * rpt;  // rows whose accumulators fit
+    w.a = static_cast<int>(lo - static_cast<int64_t>(ch) * rows);
+    w.nr = rows - w.a < per_pass ? rows - w.a : per_pass;
+    if (hi - lo < w.nr) w.nr = static_cast<int>(hi - lo);
+    lo += w.nr;
+  };
+  auto pass_of = [&](const Work& w) {
+    I8Pass ps;
+    ps.nr = w.nr;
+    if constexpr (DOWN) {
+      ps.wa = p.w + (w.e * rows + w.a) * K;
+      ps.wb = nullptr;
+    } else {
+      ps.wa = p.w + (w.e * 2 * rows + w.a) * K;
+      ps.wb = ps.wa + static_cast<int64_t>(rows) * K;
+    }
+    return ps;
+  };
+  I8Stream<NB> stream;
+  Work w;
+  w.ch = -1;
+  bool more = lo < hi;
+  if (more) {
+    next(w);
+    stream.begin(pass_of(w), K);
+  }
+  // the second launch's weights are not written by the first: they may be on
+  // their way while it ends
+  if constexpr (DOWN) griddep_wait();
   if constexpr (DOWN) {
-    // rows of dropped routes, and of tokens without any route in use
+    // rows of dropped routes, and the output where no route is in use
     if (p.clear_y) {
       for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
-        const int id = __ldg(p.ids + r);
-        if (id >= 0 && id < p.E) continue;
+        if (s.dense[r] >= 0) continue;
         for (int i = tid; i < H; i += kI8Threads) p.y[static_cast<int64_t>(r) * H + i] = 0.f;
       }
     }
@@ -525,111 +650,113 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       }
     }
   }
-  const int64_t W = static_cast<int64_t>(nc) * rows;
-  int64_t lo = W * blockIdx.x / gridDim.x;
-  const int64_t hi = W * (blockIdx.x + 1) / gridDim.x;
-  while (lo < hi) {
-    const int ch = static_cast<int>(lo / rows);
-    const int ra = static_cast<int>(lo - static_cast<int64_t>(ch) * rows);
-    const int rb = hi - lo < rows - ra ? ra + static_cast<int>(hi - lo) : rows;
-    // the chunk's expert: largest d with chunk[d] <= ch
-    int d0 = 0, d1 = s.n_experts;
-    while (d1 - d0 > 1) {
-      const int mid = (d0 + d1) >> 1;
-      if (s.chunk[mid] <= ch) d0 = mid; else d1 = mid;
-    }
-    const int first = s.off[d0] + (ch - s.chunk[d0]) * p.nt;
-    const int left = s.off[d0 + 1] - first;
-    const int cnt = left < p.nt ? left : p.nt;
-    const int64_t e = s.expert[d0];
-    I8Rows src;
-    src.absmax = nullptr;
-    src.rows = s.route + first;
-    if constexpr (DOWN) {
-      src.base = p.h;
-      src.div = 1;
-      i8_stage_rows<I8_SRC_F32>(src, cnt, K, xs, p.stride, s_max, s_scale);
-    } else {
-      src.base = p.tokens;
-      src.div = p.k;
-      i8_stage_rows<I8_SRC_BF16>(src, cnt, K, xs, p.stride, s_max, s_scale);
-    }
-    const float* ws = p.wscale + e * (DOWN ? rows : 2 * rows);
-    const int per_pass = kI8AccBytes / (64 * cnt) * rpt;
-    for (int a = ra; a < rb; a += per_pass) {
-      I8Pass ps;
-      ps.nr = rb - a < per_pass ? rb - a : per_pass;
+  int staged = -1;
+  while (more) {
+    if (w.ch != staged) {
+      staged = w.ch;
+      I8Rows src;
+      src.absmax = nullptr;
+      src.rows = s.route + w.first;
       if constexpr (DOWN) {
-        ps.wa = p.w + (e * rows + a) * K;
-        ps.wb = nullptr;
+        src.base = p.h;
+        src.div = 1;
+        i8_stage_rows<I8_SRC_F32>(src, w.cnt, K, xs, p.stride, s_max, s_scale);
       } else {
-        ps.wa = p.w + (e * 2 * rows + a) * K;
-        ps.wb = ps.wa + static_cast<int64_t>(rows) * K;
+        src.base = p.tokens;
+        src.div = p.k;
+        i8_stage_rows<I8_SRC_BF16>(src, w.cnt, K, xs, p.stride, s_max, s_scale);
       }
-      const int tiles = (ps.nr + rpt - 1) / rpt;
-      for (int i = tid; i < tiles * 16 * cnt; i += kI8Threads) acc[i] = 0;
-      __syncthreads();
-      i8_stream<NB>(ps, cnt, K, xs, p.stride, acc);
-      __syncthreads();
-      for (int i = tid; i < ps.nr * cnt; i += kI8Threads) {
-        const int j = i / ps.nr, r = i - j * ps.nr;
-        const int route = s.route[first + j];
-        if constexpr (DOWN) {
-          p.y[static_cast<int64_t>(route) * H + a + r] =
-              __fmul_rn(__fmul_rn(s_scale[j], ws[a + r]), static_cast<float>(acc[r * cnt + j]));
-        } else {
-          const int at = ((r >> 3) * 16 + (r & 7)) * cnt + j;
-          const double sx = s_scale[j];
-          const double gv = sx * ws[a + r] * acc[at];
-          const double uv = sx * ws[rows + a + r] * acc[at + 8 * cnt];
-          p.h[static_cast<int64_t>(route) * I + a + r] =
-              static_cast<float>(gv / (1.0 + exp(-gv)) * uv);
-        }
-      }
+    }
+    const int tiles = (w.nr + rpt - 1) / rpt;
+    for (int i = tid; i < tiles * 16 * w.cnt; i += kI8Threads) acc[i] = 0;
+    if (DOWN && tid < kI8DoneWords) s_done[tid] = 0u;
+    __syncthreads();
+    stream.run(w.cnt, xs, p.stride, acc);
+    const Work cur = w;
+    more = lo < hi;
+    if (more) {
+      next(w);
+      stream.begin(pass_of(w), K);
+    }
+    __syncthreads();
+    const float* ws = p.wscale + cur.e * (DOWN ? rows : 2 * rows) + cur.a;
+    for (int i = tid; i < cur.nr * cur.cnt; i += kI8Threads) {
+      const int j = i / cur.nr, r = i - j * cur.nr;
+      const int route = s.route[cur.first + j];
       if constexpr (DOWN) {
-        if (p.out) {
-          // count the rows of every touched block of output columns; whoever
-          // completes a block sums it
-          __threadfence();
-          __syncthreads();
-          const int blk0 = a / kI8CombineRows, blk1 = (a + ps.nr - 1) / kI8CombineRows;
-          for (int blk = blk0; blk <= blk1; ++blk) {
-            const int c0 = blk * kI8CombineRows;
-            const int c1 = c0 + kI8CombineRows < H ? c0 + kI8CombineRows : H;
-            if (tid == 0) {
-              const int m0 = a > c0 ? a : c0;
-              const int m1 = a + ps.nr < c1 ? a + ps.nr : c1;
-              const int old = atomicAdd(p.done + blk, m1 - m0);
-              s_last = old + (m1 - m0) == (c1 - c0) * nc;
-              if (s_last) p.done[blk] = 0;
+        p.y[static_cast<int64_t>(route) * H + cur.a + r] =
+            __fmul_rn(__fmul_rn(s_scale[j], ws[r]), static_cast<float>(acc[r * cur.cnt + j]));
+      } else {
+        const int at = ((r >> 3) * 16 + (r & 7)) * cur.cnt + j;
+        const double sx = s_scale[j];
+        const double gv = sx * ws[r] * acc[at];
+        const double uv = sx * ws[rows + r] * acc[at + 8 * cur.cnt];
+        p.h[static_cast<int64_t>(route) * I + cur.a + r] =
+            static_cast<float>(gv / (1.0 + exp(-gv)) * uv);
+      }
+    }
+    if constexpr (DOWN) {
+      if (p.out) {
+        // count the rows of every touched block of output columns; whoever
+        // completes a block sums it
+        __threadfence();
+        __syncthreads();
+        const int blk0 = cur.a / kI8CombineRows;
+        const int nblk = (cur.a + cur.nr - 1) / kI8CombineRows - blk0 + 1;
+        if (tid < nblk) {
+          const int c0 = (blk0 + tid) * kI8CombineRows;
+          const int c1 = c0 + kI8CombineRows < H ? c0 + kI8CombineRows : H;
+          const int m0 = cur.a > c0 ? cur.a : c0;
+          const int m1 = cur.a + cur.nr < c1 ? cur.a + cur.nr : c1;
+          int* const done = p.done + blk0 + tid;
+          if (atomicAdd(done, m1 - m0) + (m1 - m0) == (c1 - c0) * nc) {
+            *done = 0;
+            atomicOr(&s_done[tid >> 5], 1u << (tid & 31));
+          }
+        }
+        __syncthreads();
+        __threadfence();
+        constexpr int V = kI8CombineRows / 4;               // float4 columns of a block
+        for (int i = tid; i < nblk * p.T * V; i += kI8Threads) {
+          const int b = i / (p.T * V), rest = i - b * (p.T * V);
+          if (!(s_done[b >> 5] >> (b & 31) & 1u)) continue;
+          const int tk = rest / V, c = (blk0 + b) * kI8CombineRows + (rest - tk * V) * 4;
+          if (c >= H) continue;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float* y = p.y + static_cast<int64_t>(tk) * p.k * H + c;
+          for (int j0 = 0; j0 < p.k; j0 += 4) {
+            float4 q[4];
+            float wj[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int r = tk * p.k + j0 + j;
+              const bool live = j0 + j < p.k && s.dense[r] >= 0;
+              wj[j] = live ? __ldg(p.topk_w + r) : 0.f;
+              q[j] = live ? __ldcg(reinterpret_cast<const float4*>(
+                                y + static_cast<int64_t>(j0 + j) * H))
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            __syncthreads();
-            if (s_last) {
-              __threadfence();
-              for (int i = tid; i < p.T * kI8CombineRows; i += kI8Threads) {
-                const int tk = i / kI8CombineRows, c = c0 + i % kI8CombineRows;
-                if (c >= c1) continue;
-                float v = 0.f;
-                for (int j = 0; j < p.k; ++j) {
-                  const int r = tk * p.k + j;
-                  const int id = __ldg(p.ids + r);
-                  if (id < 0 || id >= p.E) continue;
-                  v = fmaf(__ldg(p.topk_w + r), __ldcg(p.y + static_cast<int64_t>(r) * H + c), v);
-                }
-                const int64_t o = static_cast<int64_t>(tk) * H + c;
-                if (p.out_bf16)
-                  static_cast<uint16_t*>(p.out)[o] = bf16_bits(v);
-                else
-                  static_cast<float*>(p.out)[o] = v;
-              }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v.x = fmaf(wj[j], q[j].x, v.x);
+              v.y = fmaf(wj[j], q[j].y, v.y);
+              v.z = fmaf(wj[j], q[j].z, v.z);
+              v.w = fmaf(wj[j], q[j].w, v.w);
             }
-            __syncthreads();
+          }
+          const int64_t o = static_cast<int64_t>(tk) * H + c;
+          if (p.out_bf16) {
+            uint2 b2;
+            b2.x = bf16_bits(v.x) | static_cast<uint32_t>(bf16_bits(v.y)) << 16;
+            b2.y = bf16_bits(v.z) | static_cast<uint32_t>(bf16_bits(v.w)) << 16;
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) = b2;
+          } else {
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = v;
           }
         }
       }
-      __syncthreads();
     }
-    lo += rb - ra;
+    __syncthreads();
   }
 }
 
