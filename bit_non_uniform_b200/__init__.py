@@ -410,9 +410,9 @@ def gemm_i8_workspace_size(M, N, K, epilogue=EPI_NONE) -> int:
 
 
 def gemm_i8_workspace(M, N, K, epilogue=EPI_NONE, device="cuda"):
-    """A zero-initialised workspace for cq_gemm_i8 and cq_linear_i8."""
+    """A workspace for cq_gemm_i8 and cq_linear_i8."""
     n = gemm_i8_workspace_size(M, N, K, epilogue)
-    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
 
 def _i8_product(where, x, absmax, wq, wscale, epilogue, out_dtype, out, workspace, stream):
@@ -436,7 +436,7 @@ def _i8_product(where, x, absmax, wq, wscale, epilogue, out_dtype, out, workspac
             py = _tensor("out", out, dt, shape, dev)
         need = lib().cq_gemm_i8_workspace_size(M, N, K, epilogue)
         if workspace is None and need:
-            workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         pws, nws = _scratch(workspace, dev)
         st = torch.cuda.current_stream().cuda_stream
         if absmax is not None:
@@ -471,9 +471,9 @@ def moe_i8_workspace_size(T, k, E, H, I) -> int:
 
 
 def moe_i8_workspace(T, k, E, H, I, device="cuda"):
-    """A zero-initialised workspace for cq_moe_i8."""
+    """A workspace for cq_moe_i8."""
     n = moe_i8_workspace_size(T, k, E, H, I)
-    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
 
 def cq_moe_i8(tokens, topk_ids, topk_w, w_gu, s_gu, w_dn, s_dn, out_dtype: int = F32,

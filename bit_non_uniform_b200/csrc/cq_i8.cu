@@ -11,16 +11,36 @@ namespace cq {
 
 constexpr int kI8Devices = 64;            // devices whose properties are remembered
 constexpr int64_t kI8MaxK = 131072;       // one staged row always fits shared memory
+static_assert(kI8SmemLimit - 2048 - kI8AccBytes - kI8MinSlots * kI8UnitBytes -
+                      i8_plan_bytes(kI8MaxRoutes, kI8MaxExperts) >=
+                  i8_row_stride(kI8MaxK),
+              "one row");
 
-// Shared memory left for staged rows beside the accumulators and a kernel's
-// static arrays.
-constexpr int kI8LinearRowBytes = kI8SmemLimit - 1024 - kI8AccBytes;
-constexpr int kI8MoeRowBytes =
-    kI8SmemLimit - 1024 - kI8AccBytes - static_cast<int>(sizeof(I8PlanSmem));
+// The shared memory of a streaming kernel beside its static arrays: a ring of
+// units, `tokens` staged rows, the accumulators, and (MoE) the plan.
+constexpr int kI8Smem = kI8SmemLimit - 2048;
 
-static int i8_tokens_per_pass(int64_t K, int row_bytes) {
-  const int n = row_bytes / i8_row_stride(K);
+// Tokens of one pass: as many as leave room for 12 units (96 KB: what an SM
+// needs on its way to take its share of the HBM's rate), or 8 or 4 where long
+// rows leave no room for a few tokens beside them.
+static int i8_tokens_per_pass(int64_t K, int plan) {
+  const int smem = kI8Smem - plan - kI8AccBytes, stride = i8_row_stride(K);
+  int n = (smem - 12 * kI8UnitBytes) / stride;
+  if (n < 4) n = (smem - 8 * kI8UnitBytes) / stride;
+  if (n < 1) n = (smem - kI8MinSlots * kI8UnitBytes) / stride;
   return n < kI8MaxTokens ? n : kI8MaxTokens;
+}
+
+template <typename Params>
+static int i8_layout(Params& p, int tokens, int64_t K, int plan) {
+  p.stride = i8_row_stride(K);
+  const int rest = kI8Smem - plan - kI8AccBytes - tokens * p.stride;
+  const int slots = rest / kI8UnitBytes < kI8MaxSlots ? rest / kI8UnitBytes : kI8MaxSlots;
+  p.slots = slots / kI8MinSlots * kI8MinSlots;   // a multiple of the producers, and even
+  p.xs_off = p.slots * kI8UnitBytes;
+  p.acc_off = p.xs_off + tokens * p.stride;
+  p.timeout_ns = kDefaultTimeoutNs;
+  return p.acc_off + kI8AccBytes + plan;
 }
 
 static int validate_i8(int64_t M, int64_t N, int64_t K, int epilogue, int out_dtype) {
@@ -33,34 +53,14 @@ static int validate_i8(int64_t M, int64_t N, int64_t K, int epilogue, int out_dt
   return CQ_OK;
 }
 
-template <int SRC, int NB>
-static int launch_i8_linear(const I8LinearParams& p, int grid, cudaStream_t s) {
-  static std::atomic<uint64_t> smem_set{0};
-  if (!ensure_smem_limit(i8_linear_kernel<SRC, NB>, kI8SmemLimit - 1024, smem_set))
-    return CQ_ERR_CUDA;
-  return launch_pdl(i8_linear_kernel<SRC, NB>, dim3(grid), dim3(kI8Threads),
-                    p.acc_off + kI8AccBytes, s, p);
-}
-
 template <int SRC>
 static int i8_linear(I8LinearParams p, int sms, cudaStream_t s) {
-  const int64_t M = p.M, rows = p.swiglu ? p.N / 2 : p.N;
-  const int es = SRC == I8_SRC_CODES ? 1 : 2, os = p.out_bf16 ? 2 : 4;
-  const int nt = i8_tokens_per_pass(p.K, kI8LinearRowBytes);
-  const int grid = static_cast<int>(rows < sms ? rows : sms);
-  p.stride = i8_row_stride(p.K);
-  for (int64_t m = 0; m < M; m += nt) {
-    I8LinearParams q = p;
-    q.M = static_cast<int>(M - m < nt ? M - m : nt);
-    q.x = static_cast<const uint8_t*>(p.x) + m * p.K * es;
-    q.absmax = p.absmax ? p.absmax + m : nullptr;
-    q.y = static_cast<uint8_t*>(p.y) + m * rows * os;
-    q.acc_off = q.M * p.stride;
-    const int st = q.M <= 8 ? launch_i8_linear<SRC, 1>(q, grid, s)
-                            : launch_i8_linear<SRC, 2>(q, grid, s);
-    if (st != CQ_OK) return st;
-  }
-  return CQ_OK;
+  static std::atomic<uint64_t> smem_set{0};
+  if (!ensure_smem_limit(i8_linear_kernel<SRC>, kI8Smem, smem_set)) return CQ_ERR_CUDA;
+  const int rows = p.swiglu ? p.N / 2 : p.N;
+  const int smem = i8_layout(p, p.M, p.K, 0);
+  return launch_pdl(i8_linear_kernel<SRC>, dim3(rows < sms ? rows : sms), dim3(kI8Threads), smem,
+                    s, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -74,8 +74,11 @@ struct I8TcPlan {
 
 static size_t i8_round256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Tokens up to which the product is streamed from memory.
-static bool i8_streams(int64_t M) { return M <= kI8MaxTokens; }
+// Products streamed from memory: up to 8 tokens (one block of MMA columns;
+// 6144 x 7168 with SwiGLU takes 12 us at 8 tokens and 13.5 on the tensor
+// cores, which take 16 in the same time), as long as their rows fit beside
+// the ring.
+static bool i8_streams(int64_t M, int64_t K) { return M <= 8 && M <= i8_tokens_per_pass(K, 0); }
 
 // Clusters of `s` CTAs of the split kernel that run at once (a GPC's SMs need
 // not divide evenly): asked once per device and size.
@@ -268,7 +271,7 @@ static int i8_gemm_impl(const void* x, const float* absmax, int64_t M, const int
   p.K = static_cast<int>(K);
   p.swiglu = epilogue == CQ_EPI_SWIGLU;
   p.out_bf16 = out_dtype == CQ_DTYPE_BF16;
-  if (i8_streams(M))
+  if (i8_streams(M, K))
     return codes ? i8_linear<I8_SRC_CODES>(p, sms, s) : i8_linear<I8_SRC_BF16>(p, sms, s);
   const I8TcPlan g = i8_tc_plan(M, N, K, epilogue, sms);
   if (static_cast<int64_t>(g.n_rt) * g.n_tt * g.split >= (int64_t)1 << 30)
@@ -298,7 +301,7 @@ static int i8_gemm_impl(const void* x, const float* absmax, int64_t M, const int
 // ---------------------------------------------------------------------------
 struct I8MoePlan {
   int64_t T;                 // tokens of one launch
-  size_t o_h, o_y, total;    // the counters come first
+  size_t o_y, total;         // h comes first
 };
 
 static I8MoePlan i8_moe_plan(int64_t T, int k, int64_t H, int64_t I) {
@@ -306,10 +309,7 @@ static I8MoePlan i8_moe_plan(int64_t T, int k, int64_t H, int64_t I) {
   const int64_t most = kI8MaxRoutes / k;
   m.T = T < most ? T : most;
   const size_t R = static_cast<size_t>(m.T) * k;
-  // a fixed area for the counters, so that one buffer may serve layers of
-  // different sizes: counters return to zero, and nothing else is written there
-  m.o_h = kI8MaxK / kI8CombineRows * sizeof(int);
-  m.o_y = m.o_h + i8_round256(R * I * sizeof(float));
+  m.o_y = i8_round256(R * I * sizeof(float));
   m.total = m.o_y + i8_round256(R * H * sizeof(float));
   return m;
 }
@@ -323,13 +323,10 @@ static int validate_i8_moe(int64_t T, int k, int E, int64_t H, int64_t I) {
 }
 
 template <bool DOWN, int NB>
-static int launch_i8_moe(const I8MoeParams& p, int grid, cudaStream_t s) {
+static int launch_i8_moe(const I8MoeParams& p, int grid, int smem, cudaStream_t s) {
   static std::atomic<uint64_t> smem_set{0};
-  if (!ensure_smem_limit(i8_moe_kernel<DOWN, NB>,
-                         kI8SmemLimit - 1024 - static_cast<int>(sizeof(I8PlanSmem)), smem_set))
-    return CQ_ERR_CUDA;
-  return launch_pdl(i8_moe_kernel<DOWN, NB>, dim3(grid), dim3(kI8Threads),
-                    p.acc_off + kI8AccBytes, s, p);
+  if (!ensure_smem_limit(i8_moe_kernel<DOWN, NB>, kI8Smem, smem_set)) return CQ_ERR_CUDA;
+  return launch_pdl(i8_moe_kernel<DOWN, NB>, dim3(grid), dim3(kI8Threads), smem, s, p);
 }
 
 template <bool DOWN>
@@ -338,12 +335,14 @@ static int i8_moe_stage(I8MoeParams p, const int8_t* w, const float* wscale, int
   const int64_t K = DOWN ? p.I : p.H;
   p.w = w;
   p.wscale = wscale;
-  p.stride = i8_row_stride(K);
   // an expert sees a token once as a rule: T <= 8 needs one block of columns
-  p.nt = i8_tokens_per_pass(K, kI8MoeRowBytes);
+  const int plan = i8_plan_bytes(p.R, p.E);
+  p.nt = i8_tokens_per_pass(K, plan);
   if (p.T <= 8 && p.nt > 8) p.nt = 8;
-  p.acc_off = p.nt * p.stride;
-  return p.nt <= 8 ? launch_i8_moe<DOWN, 1>(p, sms, s) : launch_i8_moe<DOWN, 2>(p, sms, s);
+  if (p.R < p.nt) p.nt = p.R;
+  const int smem = i8_layout(p, p.nt, K, plan);
+  return p.nt <= 8 ? launch_i8_moe<DOWN, 1>(p, sms, smem, s)
+                   : launch_i8_moe<DOWN, 2>(p, sms, smem, s);
 }
 
 }  // namespace cq
@@ -351,7 +350,7 @@ static int i8_moe_stage(I8MoeParams p, const int8_t* w, const float* wscale, int
 using namespace cq;
 
 extern "C" CQ_API size_t cq_gemm_i8_workspace_size(int64_t M, int64_t N, int64_t K, int epilogue) {
-  if (validate_i8(M, N, K, epilogue, CQ_DTYPE_F32) != CQ_OK || M == 0 || N == 0 || i8_streams(M))
+  if (validate_i8(M, N, K, epilogue, CQ_DTYPE_F32) != CQ_OK || M == 0 || N == 0 || i8_streams(M, K))
     return 0;
   return i8_round256(static_cast<size_t>(M) * K) + i8_round256(static_cast<size_t>(M) * sizeof(float));
 }
@@ -413,15 +412,20 @@ extern "C" CQ_API int cq_moe_i8(const uint16_t* tokens, int64_t T, const int32_t
     p.tokens = tokens + t * H;
     p.ids = topk_ids + t * k;
     p.topk_w = topk_w ? topk_w + t * k : nullptr;
-    p.h = reinterpret_cast<float*>(ws + m.o_h);
+    p.h = reinterpret_cast<float*>(ws);
     p.y = route_out ? route_out + t * k * H : reinterpret_cast<float*>(ws + m.o_y);
     p.out = out ? static_cast<uint8_t*>(out) + t * H * os : nullptr;
-    p.done = reinterpret_cast<int*>(ws);
     p.out_bf16 = out_dtype == CQ_DTYPE_BF16;
     p.clear_y = route_out != nullptr;
     st = i8_moe_stage<false>(p, w_gu, s_gu, sms, s);
     if (st != CQ_OK) return st;
     st = i8_moe_stage<true>(p, w_dn, s_dn, sms, s);
+    if (st != CQ_OK) return st;
+    if (!out) continue;
+    const int64_t n = p.T * (H / 4);
+    st = launch_pdl(i8_combine_kernel,
+                    dim3(static_cast<unsigned>((n + kI8CombineThreads - 1) / kI8CombineThreads)),
+                    dim3(kI8CombineThreads), 0, s, p);
     if (st != CQ_OK) return st;
   }
   return CQ_OK;

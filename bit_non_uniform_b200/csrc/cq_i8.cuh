@@ -8,17 +8,22 @@
 //
 // With a handful of tokens every weight byte is read once and used a handful
 // of times, so HBM bounds the kernel.  The design only serves the stream:
-//   * weight bytes go from global memory straight into the registers that
-//     mma.sync.m16n8k32 (S8) takes as its A operand, without shared memory or
-//     a barrier in between.  A dot product does not depend on the order of k,
-//     so a lane's 16 contiguous bytes serve as the k positions of two MMAs
-//     (the activations are read from shared memory under the same order);
+//   * four producer warps copy the weights into a ring of shared-memory units
+//     (16 rows x 512 bytes of K, by 16-byte asynchronous copies; a bulk copy
+//     per row took 75 cycles each and held an SM to 13 GB/s) and run on while
+//     the other 16 warps stage activations or finish a pass;
+//   * the streaming warps take the units in turn and feed them to
+//     mma.sync.m16n8k32 (S8).  A dot product does not depend on the order of k, so a lane's 16
+//     contiguous bytes serve as the k positions of two MMAs (the activations
+//     are read under the same order);
 //   * rows, not tiles, are split evenly over the CTAs (a tile's missing rows
-//     are not loaded), and inside a CTA the 256-byte steps of its rows are
-//     split evenly over the warps.  INT32 sums do not depend on their order,
-//     so the warps add their parts to the CTA's accumulators with
-//     shared-memory atomics and the result is the same on every run;
+//     are not loaded).  INT32 sums do not depend on their order, so the warps
+//     add their parts to the CTA's accumulators with shared-memory atomics and
+//     the result is the same on every run;
 //   * every CTA quantizes the few activation rows itself (no separate launch).
+// Loading straight into the consumers' registers (two buffers of 4 KB a warp)
+// kept too little in flight once several tokens made a step's arithmetic
+// longer: 4.8 TB/s at 16 tokens of 64 experts against 6.5 at 8.
 #pragma once
 
 #include "cq_device.cuh"
@@ -26,22 +31,34 @@
 
 namespace cq {
 
-constexpr int kI8Threads = 512;
-constexpr int kI8Warps = kI8Threads / 32;
-constexpr int kI8Step = 256;                 // bytes of K per step
-constexpr int kI8AccBytes = 32 * 1024;       // accumulators of one pass over the rows
+constexpr int kI8Consumers = 512;            // threads that multiply
+constexpr int kI8Warps = kI8Consumers / 32;
+constexpr int kI8Producers = 4;              // producer warps
+constexpr int kI8Threads = kI8Consumers + 32 * kI8Producers;
+constexpr int kI8Unit = 512;                 // bytes of K of a unit (16 rows)
+constexpr int kI8Pitch = kI8Unit + 64;       // 16-byte reads of two rows hit all banks
+constexpr int kI8UnitBytes = 16 * kI8Pitch;
+constexpr int kI8MaxSlots = 24;              // units in the ring
+constexpr int kI8MinSlots = 4;
+constexpr int kI8AccBytes = 16 * 1024;       // accumulators of one pass over the rows
 constexpr int kI8MaxTokens = 16;             // tokens of one pass
 constexpr int kI8MaxRoutes = 1024;           // routes of one launch of the MoE layer
 constexpr int kI8MaxExperts = 16384;
-constexpr int kI8CombineRows = 32;           // output columns of one combine block
-constexpr int kI8DoneWords = 16;              // 512 output blocks of a pass, at most
 constexpr int kI8SmemLimit = 227 * 1024;
 
-// Bytes between two activation rows in shared memory: whole steps, plus 64 so
+enum I8Site : int { SITE_I8_SLOT_EMPTY = 54, SITE_I8_SLOT_FULL = 55 };
+
+// Bytes between two activation rows in shared memory: whole units (zeros past
+// K, where a unit's weights are whatever the slot held before), plus 64 so
 // that the eight lanes of a 16-byte read phase (two rows x 64 bytes) touch
 // all 32 banks.
 __host__ __device__ constexpr int i8_row_stride(int64_t K) {
-  return static_cast<int>((K + kI8Step - 1) / kI8Step * kI8Step) + 64;
+  return static_cast<int>((K + kI8Unit - 1) / kI8Unit * kI8Unit) + 64;
+}
+
+// Barrier of the consumers.
+__device__ __forceinline__ void i8_sync() {
+  asm volatile("bar.sync 1, 512;" ::: "memory");
 }
 
 // d += A (16 x 32, row) * B (32 x 8, col), S8 x S8 -> S32.
@@ -57,11 +74,15 @@ __device__ __forceinline__ void mma_16832_s8(int (&d)[4], uint32_t a0, uint32_t 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
-// One activation code, as quant_rows_kernel decides it (FP32).
+// One activation code, as quant_rows_kernel decides it (FP32): the conversion
+// rounds to nearest even, takes NaN to 0 and saturates.
 __device__ __forceinline__ uint32_t i8_code(float v, float inv) {
-  float r = rintf(__fmul_rn(v, inv));
-  r = r > 127.f ? 127.f : (r < -127.f ? -127.f : r);
-  return static_cast<uint32_t>(static_cast<int>(r)) & 0xFFu;
+  const int r = __float2int_rn(__fmul_rn(v, inv));
+  return static_cast<uint32_t>(min(max(r, -127), 127)) & 0xFFu;
+}
+__device__ __forceinline__ uint32_t i8_code4(float a, float b, float c, float d, float inv) {
+  return __byte_perm(__byte_perm(i8_code(a, inv), i8_code(b, inv), 0x0040),
+                     __byte_perm(i8_code(c, inv), i8_code(d, inv), 0x0040), 0x5410);
 }
 
 enum I8Source : int { I8_SRC_BF16 = 0, I8_SRC_F32 = 1, I8_SRC_CODES = 2 };
@@ -71,7 +92,7 @@ enum I8Source : int { I8_SRC_BF16 = 0, I8_SRC_F32 = 1, I8_SRC_CODES = 2 };
 struct I8Rows {
   const void* base;
   const float* absmax;     // I8_SRC_CODES: the rows' maxima
-  const int* rows;         // shared memory, or null
+  const int16_t* rows;     // shared memory, or null
   int div;
 };
 
@@ -92,9 +113,9 @@ __device__ __forceinline__ void i8_load8(const void* row, int64_t k, float (&v)[
   }
 }
 
-// Quantize (or copy) `cnt` rows of K elements into shared memory, with each
-// row's RN(absmax / 127) in s_scale.  The whole CTA takes part; ends with a
-// barrier.  K is a multiple of 16.
+// Quantize (or copy) `cnt` rows of K elements into shared memory, zeros from
+// K to the end of its last unit, with each row's RN(absmax / 127) in s_scale.
+// All consumers take part; ends with their barrier.  K is a multiple of 16.
 template <int SRC>
 __device__ __forceinline__ void i8_stage_rows(const I8Rows& src, int cnt, int K, int8_t* xs,
                                               int stride, uint32_t* s_max, float* s_scale) {
@@ -104,25 +125,33 @@ __device__ __forceinline__ void i8_stage_rows(const I8Rows& src, int cnt, int K,
     const int r = src.rows ? src.rows[j] / src.div : j;
     return static_cast<const uint8_t*>(src.base) + static_cast<int64_t>(r) * K * ES;
   };
+  const int pad = (stride - 64 - K) / 16;
+  for (int i = threadIdx.x; i < cnt * pad; i += kI8Consumers) {
+    const int j = i / pad;
+    *reinterpret_cast<uint4*>(xs + j * stride + K + (i - j * pad) * 16) = make_uint4(0, 0, 0, 0);
+  }
   if constexpr (SRC == I8_SRC_CODES) {
     const int nv = K / 16;
-    for (int i = threadIdx.x; i < cnt * nv; i += kI8Threads) {
+    for (int i = threadIdx.x; i < cnt * nv; i += kI8Consumers) {
       const int j = i / nv, v = i - j * nv;
       *reinterpret_cast<uint4*>(xs + j * stride + v * 16) =
           *reinterpret_cast<const uint4*>(row_ptr(j) + v * 16);
     }
     if (threadIdx.x < cnt) s_scale[threadIdx.x] = __fdiv_rn(src.absmax[threadIdx.x], 127.0f);
-    __syncthreads();
+    i8_sync();
   } else {
     if (threadIdx.x < kI8MaxTokens) s_max[threadIdx.x] = 0u;
-    __syncthreads();
-    // each row is shared by `parts` warps
+    i8_sync();
+    // each row is shared by `parts` warps (short loops: a cold instruction
+    // cache costs a small call more than the second read of the row)
     const int parts = cnt >= kI8Warps ? 1 : kI8Warps / cnt;
-    const int nv = K / 8;
-    for (int j = warp / parts; j < cnt; j += kI8Warps / parts) {
+    const int step = parts * 32, v0 = (warp % parts) * 32 + lane, nv = K / 8;
+    const int j0 = warp / parts, dj = kI8Warps / parts;
+    for (int j = j0; j < cnt; j += dj) {
       const uint8_t* row = row_ptr(j);
       float mx = 0.f;
-      for (int v = (warp % parts) * 32 + lane; v < nv; v += parts * 32) {
+#pragma unroll 8
+      for (int v = v0; v < nv; v += step) {
         float x[8];
         i8_load8<SRC>(row, static_cast<int64_t>(v) * 8, x);
 #pragma unroll
@@ -131,162 +160,185 @@ __device__ __forceinline__ void i8_stage_rows(const I8Rows& src, int cnt, int K,
       const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
       if (lane == 0) atomicMax(&s_max[j], m);
     }
-    __syncthreads();
-    for (int j = warp / parts; j < cnt; j += kI8Warps / parts) {
+    i8_sync();
+    for (int j = j0; j < cnt; j += dj) {
       const uint8_t* row = row_ptr(j);
       const float mx = __uint_as_float(s_max[j]);
       const float inv = mx > 0.f ? __fdiv_rn(127.0f, mx) : 0.f;
-      for (int v = (warp % parts) * 32 + lane; v < nv; v += parts * 32) {
+#pragma unroll 4
+      for (int v = v0; v < nv; v += step) {
         float x[8];
         i8_load8<SRC>(row, static_cast<int64_t>(v) * 8, x);
-        uint2 q;
-        q.x = i8_code(x[0], inv) | i8_code(x[1], inv) << 8 | i8_code(x[2], inv) << 16 |
-              i8_code(x[3], inv) << 24;
-        q.y = i8_code(x[4], inv) | i8_code(x[5], inv) << 8 | i8_code(x[6], inv) << 16 |
-              i8_code(x[7], inv) << 24;
-        *reinterpret_cast<uint2*>(xs + j * stride + v * 8) = q;
+        *reinterpret_cast<uint2*>(xs + j * stride + v * 8) =
+            make_uint2(i8_code4(x[0], x[1], x[2], x[3], inv),
+                       i8_code4(x[4], x[5], x[6], x[7], inv));
       }
       if (lane == 0 && warp % parts == 0) s_scale[j] = __fdiv_rn(mx, 127.0f);
     }
-    __syncthreads();
+    i8_sync();
   }
 }
 
 // The rows one pass of a CTA multiplies: `nr` row indices from `wa`.  A tile
 // is 16 MMA rows: rows 8 t .. 8 t + 7 of `wa` and the same rows of `wb`
-// (paired: gate and up), or 16 consecutive rows of `wa` (wb == null).
+// (paired: gate and up), or 16 consecutive rows of `wa` (wb == null).  Its
+// units are 512 bytes of K each; a pass's units are numbered tile by tile.
 struct I8Pass {
   const int8_t* wa;
   const int8_t* wb;
   int nr;
+  __device__ __forceinline__ int tiles() const { return wb ? (nr + 7) >> 3 : (nr + 15) >> 4; }
 };
 
-// The multiplication of one pass.  begin() issues the warp's first loads, so
-// that they are in flight while the CTA stages activations or finishes the
-// pass before; run() adds the products of the pass's rows with the `cnt`
-// staged activation rows to acc[tile][16][cnt] (zero on entry, complete after
-// a barrier).
+// The ring of weight units in shared memory: slot q % slots holds unit q of
+// the CTA's passes, numbered through.  Unit q is copied by producer warp
+// q % kI8Producers and multiplied by streaming warp q % (slots / 2), and slots
+// is a multiple of both: a slot is always filled by one warp and emptied by
+// one warp, in order, so that a wait on its parity never meets the phase
+// before.
+struct I8Ring {
+  uint32_t data, full, empty;      // shared addresses: units, barriers
+  int slots;
+  uint64_t timeout_ns;
+  volatile int* abort_flag;
+};
+
+// Set up by one thread, before a barrier of the whole CTA.
+__device__ __forceinline__ void i8_ring_init(const I8Ring& r) {
+  for (int i = 0; i < r.slots; ++i) {
+    mbar_init(r.full + 8 * i, 32);          // the lanes of its producer
+    mbar_init(r.empty + 8 * i, 1);
+  }
+  *r.abort_flag = 0;
+  fence_mbar_init();
+}
+
+// A producer or streaming warp's place in the units: the next it handles.
+struct I8Turn {
+  uint32_t q;
+  int slot;
+  uint32_t round;
+  __device__ __forceinline__ void next(int step, int slots) {
+    q += step;
+    slot += step;
+    if (slot >= slots) {
+      slot -= slots;
+      ++round;
+    }
+  }
+};
+
+// Producer warps: copy this warp's units of the pass, whose first has number q0.
+__device__ __forceinline__ void i8_produce(const I8Ring& ring, const I8Pass& ps, int K,
+                                           uint32_t q0, I8Turn& turn) {
+  const int lane = threadIdx.x & 31;
+  const bool paired = ps.wb != nullptr;
+  const int per = paired ? 8 : 16, nk = (K + kI8Unit - 1) / kI8Unit;
+  const int total = ps.tiles() * nk;
+  int u = static_cast<int>(turn.q - q0);
+  int tile = u / nk, kk = u - tile * nk;
+  for (; u < total; u += kI8Producers) {
+    if (!wait_phase(ring.empty + 8 * turn.slot, (turn.round & 1u) ^ 1u, ring.abort_flag,
+                    ring.timeout_ns, SITE_I8_SLOT_EMPTY))
+      return;
+    const int k = kk * kI8Unit + lane * 16;
+    if (k < K) {
+      // rows 0-7 and 8-15 of the unit
+      const int left = ps.nr - tile * per, left_b = paired ? left : left - 8;
+      const int64_t at = static_cast<int64_t>(tile) * per * K + k;
+      const int8_t* a = ps.wa + at;
+      const int8_t* b = paired ? ps.wb + at : a + static_cast<int64_t>(8) * K;
+      const uint32_t dst = ring.data + turn.slot * kI8UnitBytes + lane * 16;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        if (r < left) cp_async16(dst + r * kI8Pitch, a);
+        if (r < left_b) cp_async16(dst + (8 + r) * kI8Pitch, b);
+        a += K;
+        b += K;
+      }
+    }
+    cp_async_mbar_arrive(ring.full + 8 * turn.slot);
+    turn.next(kI8Producers, ring.slots);
+    kk += kI8Producers;
+    while (kk >= nk) {
+      kk -= nk;
+      ++tile;
+    }
+  }
+}
+
+// Streaming warps: acc[tile][16][cnt] += the products of this warp's units of
+// the pass with the `cnt` staged activation rows.  acc is zero on entry and
+// complete after the consumers' barrier.  q0: the number of the pass's first
+// unit.
 template <int NB>
-struct I8Stream {
-  const int8_t *wa, *wb;    // wb == null: not paired
-  int nr, K, nk;
-  int steps;                // 256-byte steps of this warp
-  int tile, kb;             // the next step to multiply
-  int lt, lk;               // the step loaded last
-  const int8_t *pa, *pb;    // this lane's two rows of tile lt, null past the last row
-  uint4 a0[4], w0[4];
-
-  __device__ __forceinline__ void set_tile() {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int ra = lt * (wb ? 8 : 16) + g;
-    const int rb = wb ? ra : ra + 8;
-    const int8_t* base_b = wb ? wb : wa;
-    pa = ra < nr ? wa + static_cast<int64_t>(ra) * K + t * 16 : nullptr;
-    pb = rb < nr ? base_b + static_cast<int64_t>(rb) * K + t * 16 : nullptr;
-  }
-  __device__ __forceinline__ void load(uint4 (&a)[4], uint4 (&b)[4]) const {
-    const int t = threadIdx.x & 3;
+__device__ __forceinline__ void i8_consume(const I8Ring& ring, const uint8_t* ring_data,
+                                           const I8Pass& ps, int cnt, int K, const int8_t* xs,
+                                           int stride, int* acc, uint32_t q0, I8Turn& turn) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int W = ring.slots / 2;
+  if (warp >= W) return;
+  const int nk = (K + kI8Unit - 1) / kI8Unit;
+  const int total = ps.tiles() * nk;
+  const bool has0 = g < cnt, has1 = NB > 1 && g + 8 < cnt;
+  const int8_t* const x0 = xs + g * stride + t * 16;
+  const int8_t* const x1 = x0 + 8 * stride;
+  int d[NB][4], e[NB][4];                  // two chains of MMAs
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int k = lk * kI8Step + s * 64;
-      const bool in = k + t * 16 < K;
-      a[s] = in && pa ? ldg_stream16(pa + k) : make_uint4(0, 0, 0, 0);
-      b[s] = in && pb ? ldg_stream16(pb + k) : make_uint4(0, 0, 0, 0);
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[n][i] = e[n][i] = 0;
+  int u = static_cast<int>(turn.q - q0);
+  int tile = u / nk, kk = u - tile * nk;
+  for (; u < total; u += W) {
+    if (*ring.abort_flag || !wait_phase(ring.full + 8 * turn.slot, turn.round & 1u,
+                                        ring.abort_flag, ring.timeout_ns, SITE_I8_SLOT_FULL))
+      return;
+    const uint8_t* const w = ring_data + turn.slot * kI8UnitBytes + g * kI8Pitch + t * 16;
+    const int8_t* const y0 = x0 + kk * kI8Unit;
+    const int8_t* const y1 = x1 + kk * kI8Unit;
+#pragma unroll
+    for (int s = 0; s < kI8Unit / 64; ++s) {
+      const uint4 a = *reinterpret_cast<const uint4*>(w + s * 64);
+      const uint4 b = *reinterpret_cast<const uint4*>(w + 8 * kI8Pitch + s * 64);
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (has0) x = *reinterpret_cast<const uint4*>(y0 + s * 64);
+      mma_16832_s8(d[0], a.x, b.x, a.y, b.y, x.x, x.y);
+      mma_16832_s8(e[0], a.z, b.z, a.w, b.w, x.z, x.w);
+      if constexpr (NB > 1) {
+        if (cnt > 8) {
+          uint4 z = make_uint4(0, 0, 0, 0);
+          if (has1) z = *reinterpret_cast<const uint4*>(y1 + s * 64);
+          mma_16832_s8(d[1], a.x, b.x, a.y, b.y, z.x, z.y);
+          mma_16832_s8(e[1], a.z, b.z, a.w, b.w, z.z, z.w);
+        }
+      }
     }
-  }
-  __device__ __forceinline__ void advance() {
-    if (++lk == nk) {
-      lk = 0;
-      ++lt;
-      set_tile();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(ring.empty + 8 * turn.slot);
+    turn.next(W, ring.slots);
+    const int was = tile;
+    kk += W;
+    while (kk >= nk) {
+      kk -= nk;
+      ++tile;
     }
-  }
-
-  __device__ __forceinline__ void begin(const I8Pass& ps, int K_) {
-    const int warp = threadIdx.x >> 5;
-    wa = ps.wa;
-    wb = ps.wb;
-    nr = ps.nr;
-    K = K_;
-    nk = (K + kI8Step - 1) / kI8Step;
-    const int rpt = wb ? 8 : 16;
-    const int total = (nr + rpt - 1) / rpt * nk;
-    const int b0 = static_cast<int>(static_cast<int64_t>(warp) * total / kI8Warps);
-    const int b1 = static_cast<int>(static_cast<int64_t>(warp + 1) * total / kI8Warps);
-    steps = b1 - b0;
-    if (steps == 0) return;
-    lt = tile = b0 / nk;
-    lk = kb = b0 - tile * nk;
-    set_tile();
-    load(a0, w0);
-  }
-
-  __device__ __forceinline__ void run(int cnt, const int8_t* xs, int stride, int* acc) {
-    if (steps == 0) return;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    int d[NB][4];
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d[n][i] = 0;
-    auto flush = [&]() {
-      int* at = acc + tile * 16 * cnt;
+    if (tile != was || u + W >= total) {
+      // the warp's last unit of this tile
+      int* const at = acc + was * 16 * cnt;
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int col = n * 8 + 2 * t + (i & 1);
-          if (col < cnt) atomicAdd(at + (g + 8 * (i >> 1)) * cnt + col, d[n][i]);
-          d[n][i] = 0;
+          if (col < cnt) atomicAdd(at + (g + 8 * (i >> 1)) * cnt + col, d[n][i] + e[n][i]);
+          d[n][i] = e[n][i] = 0;
         }
       }
-    };
-    const bool has0 = g < cnt, has1 = NB > 1 && g + 8 < cnt;
-    const int8_t* x0 = xs + g * stride + t * 16;
-    const int8_t* x1 = xs + (g + 8) * stride + t * 16;
-    // multiply the step (tile, kb) and move on
-    auto compute = [&](const uint4 (&a)[4], const uint4 (&b)[4]) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int k = kb * kI8Step + s * 64;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (has0) x = *reinterpret_cast<const uint4*>(x0 + k);
-        mma_16832_s8(d[0], a[s].x, b[s].x, a[s].y, b[s].y, x.x, x.y);
-        mma_16832_s8(d[0], a[s].z, b[s].z, a[s].w, b[s].w, x.z, x.w);
-        if constexpr (NB > 1) {
-          if (cnt > 8) {
-            uint4 z = make_uint4(0, 0, 0, 0);
-            if (has1) z = *reinterpret_cast<const uint4*>(x1 + k);
-            mma_16832_s8(d[1], a[s].x, b[s].x, a[s].y, b[s].y, z.x, z.y);
-            mma_16832_s8(d[1], a[s].z, b[s].z, a[s].w, b[s].w, z.z, z.w);
-          }
-        }
-      }
-      if (++kb == nk) {
-        flush();
-        kb = 0;
-        ++tile;
-      }
-    };
-    // two register buffers: the next step's loads are in flight while this
-    // one is multiplied
-    uint4 a1[4], w1[4];
-    for (int b = 0; b < steps; b += 2) {
-      const bool two = b + 1 < steps;
-      if (two) {
-        advance();
-        load(a1, w1);
-      }
-      compute(a0, w0);
-      if (b + 2 < steps) {
-        advance();
-        load(a0, w0);
-      }
-      if (two) compute(a1, w1);
     }
-    if (kb != 0) flush();
   }
-};
+}
 
 // silu(g) * u with silu(g) = g / (1 + exp(-g)), in FP32.
 __device__ __forceinline__ float i8_swiglu_f32(float g, float u) {
@@ -294,7 +346,7 @@ __device__ __forceinline__ float i8_swiglu_f32(float g, float u) {
 }
 
 // ---------------------------------------------------------------------------
-// the product for at most 16 tokens
+// the product for at most 8 tokens
 // ---------------------------------------------------------------------------
 struct I8LinearParams {
   const void* x;            // bf16 [M][K], or the codes int8 [M][K]
@@ -305,25 +357,26 @@ struct I8LinearParams {
   int M, N, K;
   int swiglu, out_bf16;
   int stride;               // i8_row_stride(K)
-  int acc_off;              // bytes of the staged rows
+  int xs_off, acc_off;      // staged rows and accumulators, behind the ring
+  int slots;
+  uint64_t timeout_ns;
 };
 
-template <int SRC, int NB>
+template <int SRC>
 __global__ void __launch_bounds__(kI8Threads, 1)
     i8_linear_kernel(const __grid_constant__ I8LinearParams p) {
   extern __shared__ __align__(128) uint8_t i8_smem[];
+  __shared__ uint64_t s_bar[2 * kI8MaxSlots];
   __shared__ uint32_t s_max[kI8MaxTokens];
   __shared__ float s_scale[kI8MaxTokens];
-  int8_t* const xs = reinterpret_cast<int8_t*>(i8_smem);
+  __shared__ int s_abort;
+  int8_t* const xs = reinterpret_cast<int8_t*>(i8_smem + p.xs_off);
   int* const acc = reinterpret_cast<int*>(i8_smem + p.acc_off);
   const int tid = threadIdx.x;
   const int rows = p.swiglu ? p.N / 2 : p.N;
   const int r0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * rows / gridDim.x);
   const int r1 = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * rows / gridDim.x);
-  griddep_wait();
-  griddep_launch_dependents();
-  if (r0 >= r1) return;
-  const int rpt = p.swiglu ? 8 : 16;
+  const int rpt = p.swiglu ? 8 : 16, nk = (p.K + kI8Unit - 1) / kI8Unit;
   const int per_pass = kI8AccBytes / (64 * p.M) * rpt;      // rows whose accumulators fit
   auto pass_at = [&](int a) {
     I8Pass ps;
@@ -332,27 +385,40 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     ps.wb = p.swiglu ? ps.wa + static_cast<int64_t>(rows) * p.K : nullptr;
     return ps;
   };
-  I8Pass ps = pass_at(r0);
-  I8Stream<NB> stream;
-  stream.begin(ps, p.K);
+  const I8Ring ring = {smem_u32(i8_smem), smem_u32(s_bar), smem_u32(s_bar + kI8MaxSlots), p.slots,
+                       p.timeout_ns, &s_abort};
+  if (tid == 0) i8_ring_init(ring);
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  if (tid >= kI8Consumers) {
+    uint32_t q = 0;
+    I8Turn turn = {static_cast<uint32_t>(tid >> 5) - kI8Warps, (tid >> 5) - kI8Warps, 0u};
+    for (int a = r0; a < r1 && !*ring.abort_flag; a += per_pass) {
+      const I8Pass ps = pass_at(a);
+      i8_produce(ring, ps, p.K, q, turn);
+      q += ps.tiles() * nk;
+    }
+    cp_async_wait_all();
+    return;
+  }
   I8Rows src;
   src.base = p.x;
   src.absmax = p.absmax;
   src.rows = nullptr;
   src.div = 1;
   i8_stage_rows<SRC>(src, p.M, p.K, xs, p.stride, s_max, s_scale);
-  for (int a = r0; a < r1;) {
-    const int tiles = (ps.nr + rpt - 1) / rpt;
-    for (int i = tid; i < tiles * 16 * p.M; i += kI8Threads) acc[i] = 0;
-    __syncthreads();
-    stream.run(p.M, xs, p.stride, acc);
+  uint32_t q = 0;
+  I8Turn turn = {static_cast<uint32_t>(tid >> 5), tid >> 5, 0u};
+  for (int a = r0; a < r1; a += per_pass) {
+    const I8Pass ps = pass_at(a);
     const int nr = ps.nr;
-    if (a + nr < r1) {
-      ps = pass_at(a + nr);
-      stream.begin(ps, p.K);
-    }
-    __syncthreads();
-    for (int i = tid; i < nr * p.M; i += kI8Threads) {
+    for (int i = tid; i < ps.tiles() * 16 * p.M; i += kI8Consumers) acc[i] = 0;
+    i8_sync();
+    i8_consume<1>(ring, i8_smem, ps, p.M, p.K, xs, p.stride, acc, q, turn);
+    q += ps.tiles() * nk;
+    i8_sync();
+    for (int i = tid; i < nr * p.M; i += kI8Consumers) {
       const int m = i / nr, r = i - m * nr;
       const int at = (p.swiglu ? (r >> 3) * 16 + (r & 7) : r) * p.M + m;
       const float sx = s_scale[m];
@@ -368,27 +434,26 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       else
         static_cast<float*>(p.y)[o] = v;
     }
-    __syncthreads();
-    a += nr;
+    i8_sync();
   }
 }
 
 // ---------------------------------------------------------------------------
-// the MoE layer for a few tokens: two launches
+// the MoE layer for a few tokens: two launches, and one that sums
 // ---------------------------------------------------------------------------
-// Both launches read the routes themselves: the experts in use (ascending),
-// each with its routes, cut into chunks of at most `nt` routes.  A chunk
-// multiplies every row of its expert, so the work is chunks x rows, split
-// evenly over the CTAs.
+// Both launches read the routes themselves: the experts in use, each with its
+// routes, cut into chunks of at most `nt` routes.  A chunk multiplies every
+// row of its expert, so the work is chunks x rows, split evenly over the
+// CTAs.
 //   gate/up: xq = codes of the chunk's tokens; g, u per (row, route);
 //            h[route][row] = RN32(silu(g) u) with g, u and silu in FP64, so
 //            that the codes of the second quantization are those of any other
 //            FP64 evaluation (a value next to a rounding border would
 //            otherwise fall on either side of it);
-//   down:    hq = codes of the chunk's h rows; y[route][row], then the
-//            weighted sum over a token's routes by the CTA that completes a
-//            block of output columns (counted by rows), in the order of the
-//            token's routes: no atomics on floats, the same result every run.
+//   down:    hq = codes of the chunk's h rows; y[route][row];
+//   then a small kernel sums a token's routes in their order.  (Summed inside
+//   the second launch by whichever CTA completes a block of columns, it cost
+//   6 us a pass, or a tail of 80 us when left to the end.)
 struct I8MoeParams {
   const uint16_t* tokens;   // bf16 [T][H]
   const int32_t* ids;       // [T][k]
@@ -398,65 +463,66 @@ struct I8MoeParams {
   float* h;                 // [R][I]
   float* y;                 // [R][H]
   void* out;                // [T][H], or null
-  int* done;                // [blocks of output columns], zero between calls
   int T, k, R, E;
   int64_t H, I;
   int nt;                   // routes per chunk
   int out_bf16, clear_y;
-  int stride, acc_off;
+  int stride;               // i8_row_stride of the stage's K
+  int xs_off, acc_off;      // staged rows and accumulators, behind the ring
+  int slots;
+  uint64_t timeout_ns;
 };
 
-// Shared-memory arrays of the plan.
-struct I8PlanSmem {
-  uint32_t bits[kI8MaxExperts / 32];       // experts in use
-  int pref[kI8MaxExperts / 32 + 1];        // experts in use before each word
-  int expert[kI8MaxRoutes];                // the experts in use, ascending
-  int cnt[kI8MaxRoutes];                   // their routes
-  int off[kI8MaxRoutes + 1];               // first route of each in `route`
-  int chunk[kI8MaxRoutes + 1];             // chunks before each
-  int route[kI8MaxRoutes];                 // routes by expert
-  int16_t dense[kI8MaxRoutes];             // each route's expert, as an index into `expert`
-  int16_t rank[kI8MaxRoutes];              // its place among the expert's routes
-  int part[kI8Warps + 1];
-  int n_experts, n_chunks;
+// Arrays of the plan in shared memory, sized for the launch's routes (in
+// whole groups of 32) and experts.
+struct I8Plan {
+  uint32_t* bits;       // experts in use
+  int16_t* pref;        // experts in use before each word
+  int16_t* expert;      // the experts in use
+  int16_t* cnt;         // their routes
+  int16_t* off;         // first route of each in `route`, and the end
+  int16_t* chunk;       // chunks before each, and all
+  int16_t* route;       // routes by expert
+  int16_t* dense;       // each route's expert, as an index into `expert`, or -1
+  int16_t* rank;        // its place among the expert's routes
+  int* n;               // experts in use, chunks
 };
 
-// Exclusive prefix over v[0..n) (n <= kI8MaxRoutes) into out[0..n], whole CTA.
-template <typename F>
-__device__ __forceinline__ void i8_prefix(int n, int* out, int* part, F value) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int PER = kI8MaxRoutes / kI8Threads;
-  int v[PER], sum = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int at = threadIdx.x * PER + i;
-    v[i] = at < n ? value(at) : 0;
-    sum += v[i];
-  }
-  int inc = sum;
+__host__ __device__ constexpr int i8_plan_routes(int R) { return (R + 31) / 32 * 32; }
+__host__ __device__ constexpr int i8_plan_words(int E) { return (E + 31) / 32; }
+__host__ __device__ constexpr int i8_plan_bytes(int R, int E) {
+  return (i8_plan_words(E) * 6 + i8_plan_routes(R) * 14 + 4 * 2 + 2 * 4 + 15) / 16 * 16;
+}
+
+__device__ __forceinline__ I8Plan i8_plan_at(uint8_t* at, int R, int E) {
+  const int r = i8_plan_routes(R), w = i8_plan_words(E);
+  I8Plan s;
+  s.n = reinterpret_cast<int*>(at);
+  s.bits = reinterpret_cast<uint32_t*>(s.n + 2);
+  s.pref = reinterpret_cast<int16_t*>(s.bits + w);
+  s.expert = s.pref + w;
+  s.cnt = s.expert + r;
+  s.off = s.cnt + r;
+  s.chunk = s.off + r + 2;
+  s.route = s.chunk + r + 2;
+  s.dense = s.route + r;
+  s.rank = s.dense + r;
+  return s;
+}
+
+__device__ __forceinline__ int warp_inclusive_sum(int v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += u;
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
   }
-  if (lane == 31) part[warp] = inc;
-  __syncthreads();
-  int run = inc - sum;
-  for (int w = 0; w < warp; ++w) run += part[w];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int at = threadIdx.x * PER + i;
-    if (at < n) out[at] = run;
-    run += v[i];
-    if (at == n - 1) out[n] = run;
-  }
-  if (n == 0 && threadIdx.x == 0) out[0] = 0;
-  __syncthreads();
+  return v;
 }
 
 // The plan of at most 32 routes, by the first warp (experts in the order of
 // their first route; the order only decides which CTA works on what).
-__device__ __forceinline__ void i8_plan_small(const I8MoeParams& p, I8PlanSmem& s) {
+__device__ __forceinline__ void i8_plan_small(const I8MoeParams& p, const I8Plan& s) {
   const int lane = threadIdx.x;
   if (lane < 32) {
     int id = lane < p.R ? __ldg(p.ids + lane) : -1;
@@ -466,92 +532,98 @@ __device__ __forceinline__ void i8_plan_small(const I8MoeParams& p, I8PlanSmem& 
     const bool first = id >= 0 && (same & below) == 0;
     const unsigned firsts = __ballot_sync(0xffffffffu, first);
     const int cnt = first ? __popc(same) : 0, chunks = (cnt + p.nt - 1) / p.nt;
-    int off = cnt, ch = chunks;                  // inclusive prefixes
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, off, o), v = __shfl_up_sync(0xffffffffu, ch, o);
-      if (lane >= o) {
-        off += u;
-        ch += v;
-      }
-    }
+    const int off = warp_inclusive_sum(cnt), ch = warp_inclusive_sum(chunks);
     const int leader = __ffs(same) - 1;
     const int base = __shfl_sync(0xffffffffu, off - cnt, leader);
     const int d = __popc(firsts & ((1u << leader) - 1u));
     if (first) {
-      s.expert[d] = id;
-      s.off[d] = off - cnt;
-      s.chunk[d] = ch - chunks;
+      s.expert[d] = static_cast<int16_t>(id);
+      s.off[d] = static_cast<int16_t>(off - cnt);
+      s.chunk[d] = static_cast<int16_t>(ch - chunks);
     }
     s.dense[lane] = static_cast<int16_t>(id >= 0 ? d : -1);
-    if (id >= 0) s.route[base + __popc(same & below)] = lane;
+    if (id >= 0) s.route[base + __popc(same & below)] = static_cast<int16_t>(lane);
     if (lane == 31) {
       const int ne = __popc(firsts);
-      s.n_experts = ne;
-      s.n_chunks = ch;
-      s.off[ne] = off;
-      s.chunk[ne] = ch;
+      s.n[0] = ne;
+      s.n[1] = ch;
+      s.off[ne] = static_cast<int16_t>(off);
+      s.chunk[ne] = static_cast<int16_t>(ch);
     }
   }
   __syncthreads();
 }
 
-__device__ __forceinline__ void i8_plan(const I8MoeParams& p, I8PlanSmem& s) {
+__device__ __forceinline__ void i8_plan(const I8MoeParams& p, const I8Plan& s) {
   if (p.R <= 32) {
     i8_plan_small(p, s);
     return;
   }
   const int tid = threadIdx.x;
   const int words = (p.E + 31) / 32;
-  constexpr int PER = kI8MaxRoutes / kI8Threads;
   for (int i = tid; i < words; i += kI8Threads) s.bits[i] = 0u;
-  for (int i = tid; i < kI8MaxRoutes; i += kI8Threads) s.cnt[i] = 0;
   __syncthreads();
-  int id[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int r = tid + i * kI8Threads;
-    id[i] = r < p.R ? __ldg(p.ids + r) : -1;
-    if (id[i] >= p.E) id[i] = -1;
-    if (id[i] >= 0) atomicOr(&s.bits[id[i] >> 5], 1u << (id[i] & 31));
+  for (int r = tid; r < i8_plan_routes(p.R); r += kI8Threads) {
+    int id = r < p.R ? __ldg(p.ids + r) : -1;
+    if (id < 0 || id >= p.E) id = -1;
+    s.dense[r] = static_cast<int16_t>(id);
+    if (id >= 0) atomicOr(&s.bits[id >> 5], 1u << (id & 31));
   }
   __syncthreads();
-  i8_prefix(words, s.pref, s.part, [&](int i) { return __popc(s.bits[i]); });
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    int d = -1;
-    if (id[i] >= 0) {
-      const int w = id[i] >> 5;
-      d = s.pref[w] + __popc(s.bits[w] & ((1u << (id[i] & 31)) - 1u));
-      s.expert[d] = id[i];
-    }
-    s.dense[tid + i * kI8Threads] = static_cast<int16_t>(d);
-  }
-  if (tid == 0) s.n_experts = s.pref[words];
-  __syncthreads();
-  // each route's place among its expert's routes, in route order: every CTA
-  // of both launches has to cut an expert's routes into the same chunks
+  // the rest is short enough for one warp
   if (tid < 32) {
+    int ne = 0;
+    for (int w0 = 0; w0 < words; w0 += 32) {
+      const int n = w0 + tid < words ? __popc(s.bits[w0 + tid]) : 0;
+      const int inc = warp_inclusive_sum(n);
+      if (w0 + tid < words) s.pref[w0 + tid] = static_cast<int16_t>(ne + inc - n);
+      ne += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    for (int i = tid; i < ne; i += 32) s.cnt[i] = 0;
+    __syncwarp();
+    // each route's expert and its place among the expert's routes, in route
+    // order: every CTA of both launches has to cut an expert's routes into
+    // the same chunks
     for (int r0 = 0; r0 < p.R; r0 += 32) {
-      const int d = s.dense[r0 + tid];
+      const int id = s.dense[r0 + tid];
+      int d = -1;
+      if (id >= 0) {
+        d = s.pref[id >> 5] + __popc(s.bits[id >> 5] & ((1u << (id & 31)) - 1u));
+        s.expert[d] = static_cast<int16_t>(id);
+      }
       const unsigned same = __match_any_sync(0xffffffffu, d);
       const int before = __popc(same & ((1u << tid) - 1u));
       const int base = d >= 0 ? s.cnt[d] : 0;
       __syncwarp();
-      if (d >= 0 && before == 0) s.cnt[d] = base + __popc(same);
+      if (d >= 0 && before == 0) s.cnt[d] = static_cast<int16_t>(base + __popc(same));
+      s.dense[r0 + tid] = static_cast<int16_t>(d);
       s.rank[r0 + tid] = static_cast<int16_t>(base + before);
       __syncwarp();
     }
+    int off = 0, ch = 0;
+    for (int d0 = 0; d0 < ne; d0 += 32) {
+      const int cnt = d0 + tid < ne ? s.cnt[d0 + tid] : 0;
+      const int chunks = (cnt + p.nt - 1) / p.nt;
+      const int a = warp_inclusive_sum(cnt), b = warp_inclusive_sum(chunks);
+      if (d0 + tid < ne) {
+        s.off[d0 + tid] = static_cast<int16_t>(off + a - cnt);
+        s.chunk[d0 + tid] = static_cast<int16_t>(ch + b - chunks);
+      }
+      off += __shfl_sync(0xffffffffu, a, 31);
+      ch += __shfl_sync(0xffffffffu, b, 31);
+    }
+    if (tid == 0) {
+      s.off[ne] = static_cast<int16_t>(off);
+      s.chunk[ne] = static_cast<int16_t>(ch);
+      s.n[0] = ne;
+      s.n[1] = ch;
+    }
+    __syncwarp();
+    for (int r = tid; r < p.R; r += 32) {
+      const int d = s.dense[r];
+      if (d >= 0) s.route[s.off[d] + s.rank[r]] = static_cast<int16_t>(r);
+    }
   }
-  __syncthreads();
-  const int ne = s.n_experts;
-  i8_prefix(ne, s.off, s.part, [&](int i) { return s.cnt[i]; });
-  i8_prefix(ne, s.chunk, s.part, [&](int i) { return (s.cnt[i] + p.nt - 1) / p.nt; });
-  for (int r = tid; r < p.R; r += kI8Threads) {
-    const int d = s.dense[r];
-    if (d >= 0) s.route[s.off[d] + s.rank[r]] = r;
-  }
-  if (tid == 0) s.n_chunks = s.chunk[ne];
   __syncthreads();
 }
 
@@ -559,17 +631,22 @@ template <bool DOWN, int NB>
 __global__ void __launch_bounds__(kI8Threads, 1)
     i8_moe_kernel(const __grid_constant__ I8MoeParams p) {
   extern __shared__ __align__(128) uint8_t i8_smem[];
-  __shared__ I8PlanSmem s;
   __shared__ uint32_t s_max[kI8MaxTokens];
   __shared__ float s_scale[kI8MaxTokens];
-  __shared__ uint32_t s_done[kI8DoneWords];      // output blocks this pass completed
-  int8_t* const xs = reinterpret_cast<int8_t*>(i8_smem);
+  __shared__ uint64_t s_bar[2 * kI8MaxSlots];
+  __shared__ int s_abort;
+  int8_t* const xs = reinterpret_cast<int8_t*>(i8_smem + p.xs_off);
   int* const acc = reinterpret_cast<int*>(i8_smem + p.acc_off);
+  const I8Plan s = i8_plan_at(i8_smem + p.acc_off + kI8AccBytes, p.R, p.E);
   const int tid = threadIdx.x;
   const int H = static_cast<int>(p.H), I = static_cast<int>(p.I);
   const int K = DOWN ? I : H;
   const int rows = DOWN ? H : I;                 // rows of a chunk (gate/up: pairs)
   constexpr int rpt = DOWN ? 16 : 8;
+  const int nk = (K + kI8Unit - 1) / kI8Unit;
+  const I8Ring ring = {smem_u32(i8_smem), smem_u32(s_bar), smem_u32(s_bar + kI8MaxSlots), p.slots,
+                       p.timeout_ns, &s_abort};
+  if (tid == 0) i8_ring_init(ring);
   if constexpr (!DOWN) {
     griddep_wait();
     griddep_launch_dependents();
@@ -577,7 +654,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   // the second launch may start before the first has ended: the ids are the
   // caller's and were complete before the first began
   i8_plan(p, s);
-  const int nc = s.n_chunks;
+  const int nc = s.n[1];
   const int64_t W = static_cast<int64_t>(nc) * rows;
   int64_t lo = W * blockIdx.x / gridDim.x;       // next row of the chunks' rows
   const int64_t hi = W * (blockIdx.x + 1) / gridDim.x;
@@ -591,7 +668,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     const int ch = static_cast<int>(lo / rows);
     if (ch != w.ch) {
       // the chunk's expert: largest d with chunk[d] <= ch
-      int d0 = 0, d1 = s.n_experts;
+      int d0 = 0, d1 = s.n[0];
       while (d1 - d0 > 1) {
         const int mid = (d0 + d1) >> 1;
         if (s.chunk[mid] <= ch) d0 = mid; else d1 = mid;
@@ -620,38 +697,39 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     }
     return ps;
   };
-  I8Stream<NB> stream;
   Work w;
   w.ch = -1;
-  bool more = lo < hi;
-  if (more) {
-    next(w);
-    stream.begin(pass_of(w), K);
+  if (tid >= kI8Consumers) {
+    // the second launch's weights are not written by the first: the ring may
+    // fill while that ends
+    uint32_t q = 0;
+    I8Turn turn = {static_cast<uint32_t>(tid >> 5) - kI8Warps, (tid >> 5) - kI8Warps, 0u};
+    while (lo < hi && !*ring.abort_flag) {
+      next(w);
+      const I8Pass ps = pass_of(w);
+      i8_produce(ring, ps, K, q, turn);
+      q += ps.tiles() * nk;
+    }
+    cp_async_wait_all();
+    return;
   }
-  // the second launch's weights are not written by the first: they may be on
-  // their way while it ends
-  if constexpr (DOWN) griddep_wait();
   if constexpr (DOWN) {
-    // rows of dropped routes, and the output where no route is in use
+    griddep_wait();
+    griddep_launch_dependents();
+    // rows of dropped routes
     if (p.clear_y) {
       for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
         if (s.dense[r] >= 0) continue;
-        for (int i = tid; i < H; i += kI8Threads) p.y[static_cast<int64_t>(r) * H + i] = 0.f;
-      }
-    }
-    if (nc == 0 && p.out) {
-      const int64_t n = static_cast<int64_t>(p.T) * H;
-      for (int64_t i = static_cast<int64_t>(blockIdx.x) * kI8Threads + tid; i < n;
-           i += static_cast<int64_t>(gridDim.x) * kI8Threads) {
-        if (p.out_bf16)
-          static_cast<uint16_t*>(p.out)[i] = 0;
-        else
-          static_cast<float*>(p.out)[i] = 0.f;
+        for (int i = tid; i < H; i += kI8Consumers) p.y[static_cast<int64_t>(r) * H + i] = 0.f;
       }
     }
   }
   int staged = -1;
-  while (more) {
+  uint32_t q = 0;
+  I8Turn turn = {static_cast<uint32_t>(tid >> 5), tid >> 5, 0u};
+  while (lo < hi) {
+    next(w);
+    const I8Pass ps = pass_of(w);
     if (w.ch != staged) {
       staged = w.ch;
       I8Rows src;
@@ -667,96 +745,71 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         i8_stage_rows<I8_SRC_BF16>(src, w.cnt, K, xs, p.stride, s_max, s_scale);
       }
     }
-    const int tiles = (w.nr + rpt - 1) / rpt;
-    for (int i = tid; i < tiles * 16 * w.cnt; i += kI8Threads) acc[i] = 0;
-    if (DOWN && tid < kI8DoneWords) s_done[tid] = 0u;
-    __syncthreads();
-    stream.run(w.cnt, xs, p.stride, acc);
-    const Work cur = w;
-    more = lo < hi;
-    if (more) {
-      next(w);
-      stream.begin(pass_of(w), K);
-    }
-    __syncthreads();
-    const float* ws = p.wscale + cur.e * (DOWN ? rows : 2 * rows) + cur.a;
-    for (int i = tid; i < cur.nr * cur.cnt; i += kI8Threads) {
-      const int j = i / cur.nr, r = i - j * cur.nr;
-      const int route = s.route[cur.first + j];
+    for (int i = tid; i < ps.tiles() * 16 * w.cnt; i += kI8Consumers) acc[i] = 0;
+    i8_sync();
+    i8_consume<NB>(ring, i8_smem, ps, w.cnt, K, xs, p.stride, acc, q, turn);
+    q += ps.tiles() * nk;
+    i8_sync();
+    const float* ws = p.wscale + w.e * (DOWN ? rows : 2 * rows) + w.a;
+    for (int i = tid; i < w.nr * w.cnt; i += kI8Consumers) {
+      const int j = i / w.nr, r = i - j * w.nr;
+      const int route = s.route[w.first + j];
       if constexpr (DOWN) {
-        p.y[static_cast<int64_t>(route) * H + cur.a + r] =
-            __fmul_rn(__fmul_rn(s_scale[j], ws[r]), static_cast<float>(acc[r * cur.cnt + j]));
+        p.y[static_cast<int64_t>(route) * H + w.a + r] =
+            __fmul_rn(__fmul_rn(s_scale[j], ws[r]), static_cast<float>(acc[r * w.cnt + j]));
       } else {
-        const int at = ((r >> 3) * 16 + (r & 7)) * cur.cnt + j;
+        const int at = ((r >> 3) * 16 + (r & 7)) * w.cnt + j;
         const double sx = s_scale[j];
         const double gv = sx * ws[r] * acc[at];
-        const double uv = sx * ws[rows + r] * acc[at + 8 * cur.cnt];
-        p.h[static_cast<int64_t>(route) * I + cur.a + r] =
+        const double uv = sx * ws[rows + r] * acc[at + 8 * w.cnt];
+        p.h[static_cast<int64_t>(route) * I + w.a + r] =
             static_cast<float>(gv / (1.0 + exp(-gv)) * uv);
       }
     }
-    if constexpr (DOWN) {
-      if (p.out) {
-        // count the rows of every touched block of output columns; whoever
-        // completes a block sums it
-        __threadfence();
-        __syncthreads();
-        const int blk0 = cur.a / kI8CombineRows;
-        const int nblk = (cur.a + cur.nr - 1) / kI8CombineRows - blk0 + 1;
-        if (tid < nblk) {
-          const int c0 = (blk0 + tid) * kI8CombineRows;
-          const int c1 = c0 + kI8CombineRows < H ? c0 + kI8CombineRows : H;
-          const int m0 = cur.a > c0 ? cur.a : c0;
-          const int m1 = cur.a + cur.nr < c1 ? cur.a + cur.nr : c1;
-          int* const done = p.done + blk0 + tid;
-          if (atomicAdd(done, m1 - m0) + (m1 - m0) == (c1 - c0) * nc) {
-            *done = 0;
-            atomicOr(&s_done[tid >> 5], 1u << (tid & 31));
-          }
-        }
-        __syncthreads();
-        __threadfence();
-        constexpr int V = kI8CombineRows / 4;               // float4 columns of a block
-        for (int i = tid; i < nblk * p.T * V; i += kI8Threads) {
-          const int b = i / (p.T * V), rest = i - b * (p.T * V);
-          if (!(s_done[b >> 5] >> (b & 31) & 1u)) continue;
-          const int tk = rest / V, c = (blk0 + b) * kI8CombineRows + (rest - tk * V) * 4;
-          if (c >= H) continue;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          const float* y = p.y + static_cast<int64_t>(tk) * p.k * H + c;
-          for (int j0 = 0; j0 < p.k; j0 += 4) {
-            float4 q[4];
-            float wj[4];
+    i8_sync();
+  }
+}
+
+// out[t][c] = sum_j w[t][j] y[t k + j][c] (j ascending, FP32; dropped routes
+// contribute nothing): one float4 of columns per thread.
+constexpr int kI8CombineThreads = 128;
+
+__global__ void __launch_bounds__(kI8CombineThreads)
+    i8_combine_kernel(const __grid_constant__ I8MoeParams p) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kI8CombineThreads + threadIdx.x;
+  const int V = static_cast<int>(p.H / 4);
+  griddep_wait();
+  griddep_launch_dependents();
+  if (i >= static_cast<int64_t>(p.T) * V) return;
+  const int t = static_cast<int>(i / V), c = static_cast<int>(i - static_cast<int64_t>(t) * V);
+  const float4* y = reinterpret_cast<const float4*>(p.y) + static_cast<int64_t>(t) * p.k * V + c;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = 0; j0 < p.k; j0 += 8) {
+    float4 q[8];
+    float wj[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int r = tk * p.k + j0 + j;
-              const bool live = j0 + j < p.k && s.dense[r] >= 0;
-              wj[j] = live ? __ldg(p.topk_w + r) : 0.f;
-              q[j] = live ? __ldcg(reinterpret_cast<const float4*>(
-                                y + static_cast<int64_t>(j0 + j) * H))
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              v.x = fmaf(wj[j], q[j].x, v.x);
-              v.y = fmaf(wj[j], q[j].y, v.y);
-              v.z = fmaf(wj[j], q[j].z, v.z);
-              v.w = fmaf(wj[j], q[j].w, v.w);
-            }
-          }
-          const int64_t o = static_cast<int64_t>(tk) * H + c;
-          if (p.out_bf16) {
-            uint2 b2;
-            b2.x = bf16_bits(v.x) | static_cast<uint32_t>(bf16_bits(v.y)) << 16;
-            b2.y = bf16_bits(v.z) | static_cast<uint32_t>(bf16_bits(v.w)) << 16;
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) = b2;
-          } else {
-            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = v;
-          }
-        }
-      }
+    for (int j = 0; j < 8; ++j) {
+      const int r = t * p.k + j0 + j;
+      const int id = j0 + j < p.k ? __ldg(p.ids + r) : -1;
+      const bool live = id >= 0 && id < p.E;
+      wj[j] = live ? __ldg(p.topk_w + r) : 0.f;
+      q[j] = live ? __ldcg(y + static_cast<int64_t>(j0 + j) * V) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v.x = fmaf(wj[j], q[j].x, v.x);
+      v.y = fmaf(wj[j], q[j].y, v.y);
+      v.z = fmaf(wj[j], q[j].z, v.z);
+      v.w = fmaf(wj[j], q[j].w, v.w);
+    }
+  }
+  if (p.out_bf16) {
+    uint2 b;
+    b.x = bf16_bits(v.x) | static_cast<uint32_t>(bf16_bits(v.y)) << 16;
+    b.y = bf16_bits(v.z) | static_cast<uint32_t>(bf16_bits(v.w)) << 16;
+    static_cast<uint2*>(p.out)[i] = b;
+  } else {
+    static_cast<float4*>(p.out)[i] = v;
   }
 }
 

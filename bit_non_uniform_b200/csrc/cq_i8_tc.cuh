@@ -740,8 +740,7 @@ __global__ void __launch_bounds__(kQvThreads)
   mx = __uint_as_float(mb);
   const float inv = mx > 0.f ? __fdiv_rn(127.0f, mx) : 0.f;
   auto code4 = [&](uint32_t a, uint32_t b) {
-    return i8_code(bf16_lo(a), inv) | i8_code(bf16_hi(a), inv) << 8 |
-           i8_code(bf16_lo(b), inv) << 16 | i8_code(bf16_hi(b), inv) << 24;
+    return i8_code4(bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b), inv);
   };
 #pragma unroll
   for (int i = 0; i < kQvKeep; ++i) {

@@ -346,7 +346,7 @@ CQ_API int cq_linear_i8(const uint16_t *x, int64_t M, const int8_t *wq, const fl
 /*
  * cq_moe_i8 -- the routed-expert FFN of one MoE layer with INT8 experts, for
  * a few tokens (a decode step): two kernels that read each expert in use
- * once.  For every route r = t*k + j with e = topk_ids[t][j]:
+ * once, and one that sums each token's routes.  For every route r = t*k + j with e = topk_ids[t][j]:
  *   xq, absmax = cq_quant_rows(tokens[t]);
  *   g|u   = RN(absmax / 127) * s_gu[e][n] * (xq . w_gu[e][n])
  *   h     = RN32(silu(g) * u), evaluated in FP64 so that the codes of
@@ -363,8 +363,7 @@ CQ_API int cq_linear_i8(const uint16_t *x, int64_t M, const int8_t *wq, const fl
  *   route_out float [T*k][H] per-route outputs (may be NULL)
  *   out       [T][H] in out_dtype (may be NULL)
  *   workspace device scratch of cq_moe_i8_workspace_size(...) bytes, 256-byte
- *             aligned, zero before the first call that uses it; every
- *             completed call leaves its counters zero
+ *             aligned
  * A shared expert of the same width is one more expert: id E-1 and weight 1
  * in an extra column of topk_ids.  H and I multiples of 16, at most 131072;
  * k at most 1024; E at most 16384.  More than 1024 routes run as successive

@@ -105,6 +105,9 @@ PRODUCTS = [
     (300,   1003, 2048, False, False),
     (1025,  514,  784,  True,  True),
     (2049,  1281, 96,   False, False),
+    (16,  300,  8208, False, False),       # long rows staged for 16, 11 and 2 tokens
+    (11,  40,   14000, True, False),
+    (2,   100,  99984, False, False),
 ]
 
 
@@ -240,6 +243,9 @@ MOE = [
     (300, 5, 7,  48,   32,  0.1, False),      # more routes than one group holds
     (2,   3, 3,  16,   4096, 0.0, False),
     (20,  1, 1,  16400, 32, 0.0, False),      # long rows: fewer tokens per pass
+    (16,  4, 5,  7168, 48,  0.0, False),      # 16 staged tokens leave a short ring
+    (14,  3, 4,  64,   8208, 0.3, False),
+    (9,   2, 3,  9216, 9232, 0.0, True),
 ]
 
 
