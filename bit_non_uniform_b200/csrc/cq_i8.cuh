@@ -307,12 +307,10 @@ __device__ __forceinline__ void i8_consume(const I8Ring& ring, const uint8_t* ri
       mma_16832_s8(d[0], a.x, b.x, a.y, b.y, x.x, x.y);
       mma_16832_s8(e[0], a.z, b.z, a.w, b.w, x.z, x.w);
       if constexpr (NB > 1) {
-        if (cnt > 8) {
-          uint4 z = make_uint4(0, 0, 0, 0);
-          if (has1) z = *reinterpret_cast<const uint4*>(y1 + s * 64);
-          mma_16832_s8(d[1], a.x, b.x, a.y, b.y, z.x, z.y);
-          mma_16832_s8(e[1], a.z, b.z, a.w, b.w, z.z, z.w);
-        }
+        uint4 z = make_uint4(0, 0, 0, 0);
+        if (has1) z = *reinterpret_cast<const uint4*>(y1 + s * 64);
+        mma_16832_s8(d[1], a.x, b.x, a.y, b.y, z.x, z.y);
+        mma_16832_s8(e[1], a.z, b.z, a.w, b.w, z.z, z.w);
       }
     }
     __syncwarp();
@@ -747,7 +745,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     }
     for (int i = tid; i < ps.tiles() * 16 * w.cnt; i += kI8Consumers) acc[i] = 0;
     i8_sync();
-    i8_consume<NB>(ring, i8_smem, ps, w.cnt, K, xs, p.stride, acc, q, turn);
+    if (NB > 1 && w.cnt > 8)
+      i8_consume<NB>(ring, i8_smem, ps, w.cnt, K, xs, p.stride, acc, q, turn);
+    else
+      i8_consume<1>(ring, i8_smem, ps, w.cnt, K, xs, p.stride, acc, q, turn);
     q += ps.tiles() * nk;
     i8_sync();
     const float* ws = p.wscale + w.e * (DOWN ? rows : 2 * rows) + w.a;
