@@ -361,48 +361,59 @@ def cq_moe_grouped_gemm(tokens, topk_ids, topk_w, layer, E: int, H: int, I: int,
 # ---------------------------------------------------------------------------
 # INT8 weights
 # ---------------------------------------------------------------------------
-_NULL = contextlib.nullcontext()
-
-
-def _on_device(t, stream):
+# A decode step makes many of these calls, each a few microseconds long on the
+# GPU, so the host side of a call is kept short: one test per tensor, the
+# current stream's handle without a Stream object, and no context manager
+# where the call's device and stream are the current ones already.
+def _on_device(index: int, stream):
     """The call's device and stream as the current ones (libcq launches on the
     current device)."""
-    if t.device.index == torch.cuda.current_device():
-        return _NULL if stream is None else torch.cuda.stream(stream)
     stack = contextlib.ExitStack()
-    stack.enter_context(torch.cuda.device(t.device))
+    stack.enter_context(torch.cuda.device(index))
     if stream is not None:
         stack.enter_context(torch.cuda.stream(stream))
     return stack
 
 
-def _tensor(name, t, dtype, shape, device):
+def _elsewhere(index: int, stream) -> bool:
+    return stream is not None or index != torch._C._cuda_getDevice()
+
+
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _tensor(name, t, dtype, shape, index: int) -> int:
     """Check one argument of a call and return its address."""
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        return t.data_ptr()
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.dtype != dtype:
         raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _scratch(workspace, device):
+def _scratch(workspace, index: int):
     """(address, bytes) of a call's workspace."""
     if workspace is None:
         return None, 0
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"the workspace must be contiguous on {device}")
-    n = workspace.numel() * workspace.element_size()
-    return workspace.data_ptr(), n
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous on cuda:{index}")
+    return workspace.data_ptr(), workspace.nbytes
+
+
+_DTYPES = {F32: torch.float32, BF16: torch.bfloat16}
 
 
 def _out_dtype(out_dtype: int):
-    if out_dtype not in (F32, BF16):
+    dt = _DTYPES.get(out_dtype)
+    if dt is None:
         raise ValueError(f"out_dtype must be F32 or BF16, not {out_dtype!r}")
-    return torch.float32 if out_dtype == F32 else torch.bfloat16
+    return dt
 
 
 def gemm_i8_workspace_size(M, N, K, epilogue=EPI_NONE) -> int:
@@ -419,33 +430,35 @@ def _i8_product(where, x, absmax, wq, wscale, epilogue, out_dtype, out, workspac
     if x.dim() != 2 or wq.dim() != 2:
         raise ValueError(f"{where}: activations [M][K] and weights [N][K] expected")
     _need_cuda(x)
-    dev = x.device
+    index = x.get_device()
+    if _elsewhere(index, stream):
+        with _on_device(index, stream):
+            return _i8_product(where, x, absmax, wq, wscale, epilogue, out_dtype, out, workspace,
+                               None)
+    L = lib()
     M, K = x.shape
     N = wq.shape[0]
     dt = _out_dtype(out_dtype)
-    px = _tensor("xq" if absmax is not None else "x", x,
-                 torch.int8 if absmax is not None else torch.bfloat16, (M, K), dev)
-    pw = _tensor("wq", wq, torch.int8, (N, K), dev)
-    ps = _tensor("wscale", wscale, torch.float32, (N,), dev)
+    px = _tensor("x", x, torch.bfloat16 if absmax is None else torch.int8, (M, K), index)
+    pw = _tensor("wq", wq, torch.int8, (N, K), index)
+    ps = _tensor("wscale", wscale, torch.float32, (N,), index)
     shape = (M, N // 2 if epilogue == EPI_SWIGLU else N)
-    with _on_device(x, stream):
-        if out is None:
-            out = torch.empty(shape, dtype=dt, device=dev)
-            py = out.data_ptr()
-        else:
-            py = _tensor("out", out, dt, shape, dev)
-        need = lib().cq_gemm_i8_workspace_size(M, N, K, epilogue)
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        pws, nws = _scratch(workspace, dev)
-        st = torch.cuda.current_stream().cuda_stream
-        if absmax is not None:
-            pa = _tensor("absmax", absmax, torch.float32, (M,), dev)
-            _check(lib().cq_gemm_i8(px, pa, M, pw, ps, N, K, epilogue, out_dtype, py, pws, nws,
-                                    st), where)
-        else:
-            _check(lib().cq_linear_i8(px, M, pw, ps, N, K, epilogue, out_dtype, py, pws, nws,
-                                      st), where)
+    if out is None:
+        out = x.new_empty(shape, dtype=dt)
+        py = out.data_ptr()
+    else:
+        py = _tensor("out", out, dt, shape, index)
+    st = _raw_stream(index)
+    if absmax is not None:
+        pa = _tensor("absmax", absmax, torch.float32, (M,), index)
+        _check(L.cq_gemm_i8(px, pa, M, pw, ps, N, K, epilogue, out_dtype, py, None, 0, st), where)
+        return out
+    if workspace is None:
+        need = L.cq_gemm_i8_workspace_size(M, N, K, epilogue)
+        if need:
+            workspace = x.new_empty(need, dtype=torch.uint8)
+    pws, nws = _scratch(workspace, index)
+    _check(L.cq_linear_i8(px, M, pw, ps, N, K, epilogue, out_dtype, py, pws, nws, st), where)
     return out
 
 
@@ -485,37 +498,42 @@ def cq_moe_i8(tokens, topk_ids, topk_w, w_gu, s_gu, w_dn, s_dn, out_dtype: int =
         raise ValueError("cq_moe_i8: tokens [T][H], topk_ids [T][k], w_gu [E][2I][H] and "
                          "w_dn [E][H][I] expected")
     _need_cuda(tokens)
-    dev = tokens.device
+    index = tokens.get_device()
+    if _elsewhere(index, stream):
+        with _on_device(index, stream):
+            return cq_moe_i8(tokens, topk_ids, topk_w, w_gu, s_gu, w_dn, s_dn, out_dtype,
+                             route_out, combine, workspace)
+    L = lib()
     T, H = tokens.shape
     k = topk_ids.shape[1]
     E, _, I = w_dn.shape
     dt = _out_dtype(out_dtype)
-    pt = _tensor("tokens", tokens, torch.bfloat16, (T, H), dev)
-    pi = _tensor("topk_ids", topk_ids, torch.int32, (T, k), dev)
+    pt = _tensor("tokens", tokens, torch.bfloat16, (T, H), index)
+    pi = _tensor("topk_ids", topk_ids, torch.int32, (T, k), index)
     if topk_w is None and combine:
         raise ValueError("cq_moe_i8 needs topk_w to combine the routes")
-    pk = None if topk_w is None else _tensor("topk_w", topk_w, torch.float32, (T, k), dev)
-    pgu = _tensor("w_gu", w_gu, torch.int8, (E, 2 * I, H), dev)
-    psg = _tensor("s_gu", s_gu, torch.float32, (E, 2 * I), dev)
-    pdn = _tensor("w_dn", w_dn, torch.int8, (E, H, I), dev)
-    psd = _tensor("s_dn", s_dn, torch.float32, (E, H), dev)
-    with _on_device(tokens, stream):
-        ro = pro = None
-        if route_out is True:
-            ro = torch.empty((T * k, H), dtype=torch.float32, device=dev)
-            pro = ro.data_ptr()
-        elif route_out is not None and route_out is not False:
-            ro = route_out
-            pro = _tensor("route_out", ro, torch.float32, (T * k, H), dev)
-        out = po = None
-        if combine:
-            out = torch.empty((T, H), dtype=dt, device=dev)
-            po = out.data_ptr()
-        if workspace is None:
-            workspace = moe_i8_workspace(T, k, E, H, I, dev)
-        pws, nws = _scratch(workspace, dev)
-        _check(lib().cq_moe_i8(pt, T, pi, pk, k, E, pgu, psg, pdn, psd, H, I, out_dtype, pro, po,
-                               pws, nws, torch.cuda.current_stream().cuda_stream), "cq_moe_i8")
+    pk = None if topk_w is None else _tensor("topk_w", topk_w, torch.float32, (T, k), index)
+    pgu = _tensor("w_gu", w_gu, torch.int8, (E, 2 * I, H), index)
+    psg = _tensor("s_gu", s_gu, torch.float32, (E, 2 * I), index)
+    pdn = _tensor("w_dn", w_dn, torch.int8, (E, H, I), index)
+    psd = _tensor("s_dn", s_dn, torch.float32, (E, H), index)
+    ro = pro = None
+    if route_out is True:
+        ro = tokens.new_empty((T * k, H), dtype=torch.float32)
+        pro = ro.data_ptr()
+    elif route_out is not None and route_out is not False:
+        ro = route_out
+        pro = _tensor("route_out", ro, torch.float32, (T * k, H), index)
+    out = po = None
+    if combine:
+        out = tokens.new_empty((T, H), dtype=dt)
+        po = out.data_ptr()
+    if workspace is None:
+        need = L.cq_moe_i8_workspace_size(T, k, E, H, I)
+        workspace = tokens.new_empty(max(need, 256), dtype=torch.uint8)
+    pws, nws = _scratch(workspace, index)
+    _check(L.cq_moe_i8(pt, T, pi, pk, k, E, pgu, psg, pdn, psd, H, I, out_dtype, pro, po, pws, nws,
+                       _raw_stream(index)), "cq_moe_i8")
     return ro, out
 
 
@@ -526,19 +544,22 @@ def cq_moe_route(logits, k: int, bias=None, scoring: int = SCORE_SOFTMAX, renorm
     if logits.dim() != 2:
         raise ValueError("cq_moe_route: logits [T][E] expected")
     _need_cuda(logits)
-    if logits.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"logits are {logits.dtype}, expected float32 or bfloat16")
-    dev = logits.device
+    dt = logits.dtype
+    if dt is not torch.float32 and dt is not torch.bfloat16:
+        raise ValueError(f"logits are {dt}, expected float32 or bfloat16")
+    index = logits.get_device()
+    if _elsewhere(index, stream):
+        with _on_device(index, stream):
+            return cq_moe_route(logits, k, bias, scoring, renorm, scale)
     T, E = logits.shape
-    pl = _tensor("logits", logits, logits.dtype, (T, E), dev)
-    pb = None if bias is None else _tensor("bias", bias, torch.float32, (E,), dev)
-    with _on_device(logits, stream):
-        ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
-        w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
-        _check(lib().cq_moe_route(pl, BF16 if logits.dtype == torch.bfloat16 else F32, T, E, k,
-                                  pb, scoring, 1 if renorm else 0, scale, ids.data_ptr(),
-                                  w.data_ptr(), torch.cuda.current_stream().cuda_stream),
-               "cq_moe_route")
+    pl = _tensor("logits", logits, dt, (T, E), index)
+    pb = None if bias is None else _tensor("bias", bias, torch.float32, (E,), index)
+    shape = (T, max(k, 0))
+    ids = logits.new_empty(shape, dtype=torch.int32)
+    w = logits.new_empty(shape, dtype=torch.float32)
+    _check(lib().cq_moe_route(pl, F32 if dt is torch.float32 else BF16, T, E, k, pb, scoring,
+                              1 if renorm else 0, scale, ids.data_ptr(), w.data_ptr(),
+                              _raw_stream(index)), "cq_moe_route")
     return ids, w
 
 
