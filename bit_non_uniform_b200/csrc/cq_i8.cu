@@ -68,8 +68,9 @@ static int i8_linear(I8LinearParams p, int sms, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 struct I8TcPlan {
   bool pair;
-  int NT, rows, split;       // tokens and weight rows of a CTA's tile, CTAs per tile
+  int NT, split;             // tokens of a tile, CTAs per tile (split kernel)
   int n_rt, n_tt, nkb;
+  int main_tiles, cut;       // pair kernel: whole tiles, parts of the others
 };
 
 static size_t i8_round256(size_t v) { return (v + 255) / 256 * 256; }
@@ -107,47 +108,56 @@ static int i8_clusters_at_once(int s, int sms) {
   return n;
 }
 
-// Cycles of one K block of a tile: the MMAs (128 rows x nt tokens per SM), or
-// the block's bytes at about 40 per cycle and SM.
+// The cheapest kernel and tile by an estimate in cycles.  A block of K of a
+// CTA takes the time of its MMAs (2 cycles per token) or of its copies; a
+// launch at least the weights' time in HBM (about 3400 bytes a cycle).  The
+// copies were measured at 520 cycles a block for 20 KB, 560 for 24 KB and 625
+// for 32 KB with all SMs reading (11 to 13 TB/s out of L2: giving the
+// activations a producer warp of their own changed nothing).  Over sweeps at
+// 24 to 4096 tokens of 6144 x 7168, 7168 x 2048 and 2048 x 7168 the choice is
+// within 10% of the best tile and split; tiles of fewer than 128 rows never won.
 static int64_t i8_block_cost(int nt, int rows_loaded) {
-  const int64_t mma = 2 * nt, bytes = rows_loaded * kTcBlock / 40;
-  return mma > bytes ? mma : bytes;
+  const int64_t mma = 2 * nt, copies = 340 + rows_loaded * kTcBlock / 115;
+  return mma > copies ? mma : copies;
 }
 
-// The cheapest kernel and tile by an estimate in cycles: rounds of tiles over
-// the SMs x K blocks per CTA x the cost of a block, and a constant for the
-// cluster's sum.
 static I8TcPlan i8_tc_plan(int64_t M, int64_t N, int64_t K, int epilogue, int sms) {
   const bool sw = epilogue == CQ_EPI_SWIGLU;
   const int64_t out = sw ? N / 2 : N;
-  const int64_t nkb = (K + kTcBlock - 1) / kTcBlock;
+  const int64_t nkb = (K + kTcBlock - 1) / kTcBlock, hbm = N * K / 3400;
   I8TcPlan best = {};
   int64_t cost = INT64_MAX;
-  auto consider = [&](bool pair, int nt, int rows, int split, int64_t n_rt, int64_t n_tt,
-                      int64_t c) {
+  auto consider = [&](bool pair, int nt, int split, int64_t n_rt, int64_t n_tt, int64_t main,
+                      int cut, int64_t c) {
     if (c >= cost) return;
     cost = c;
-    best = {pair, nt, rows, split, static_cast<int>(n_rt), static_cast<int>(n_tt),
-            static_cast<int>(nkb)};
+    best = {pair, nt, split, static_cast<int>(n_rt), static_cast<int>(n_tt),
+            static_cast<int>(nkb), static_cast<int>(main), cut};
   };
+  const int64_t per2 = sw ? kRows : 2 * kRows, n_rt2 = (out + per2 - 1) / per2;
+  const int64_t units = sms / 2;
   for (int nt = 256; nt >= 128; nt -= 32) {
-    const int64_t per = sw ? kRows : 2 * kRows;
-    const int64_t n_rt = (out + per - 1) / per, n_tt = (M + nt - 1) / nt;
-    const int64_t rounds = (n_rt * n_tt + sms / 2 - 1) / (sms / 2);
-    consider(true, nt, kRows, 1, n_rt, n_tt,
-             rounds * nkb * i8_block_cost(nt, kRows + nt / 2) + 6000);
+    const int64_t n_tt = (M + nt - 1) / nt, tiles = n_rt2 * n_tt;
+    const int64_t block = i8_block_cost(nt, kRows + nt / 2);
+    const int64_t main = tiles / units * units;
+    for (int cut = 1; cut <= 4; cut *= 2) {
+      if (nt / cut % 32 != 0) break;
+      const int64_t rest = ((tiles - main) * cut + units - 1) / units;
+      int64_t c = main / units * nkb * block +
+                  rest * nkb * i8_block_cost(nt / cut, kRows + nt / cut / 2);
+      c = (c > hbm ? c : hbm) + 16000 + 16 * (nt / cut);
+      consider(true, nt, 1, n_rt2, n_tt, main, cut, c);
+    }
   }
+  const int64_t per = sw ? kRows / 2 : kRows, n_rt = (out + per - 1) / per;
   for (int nt = 32; nt <= 128; nt *= 2) {
-    for (int rows = kRows; rows >= 32; rows -= 16) {
-      const int64_t per = sw ? rows / 2 : rows;
-      const int64_t n_rt = (out + per - 1) / per, n_tt = (M + nt - 1) / nt;
-      for (int s = 1; s <= kTcMaxSplit && s <= nkb; ++s) {
-        const int at_once = i8_clusters_at_once(s, sms);
-        const int64_t rounds = (n_rt * n_tt + at_once - 1) / at_once;
-        const int64_t each =
-            (nkb + s - 1) / s * i8_block_cost(nt, rows + nt) + 3000 + (s > 1 ? 2000 : 0);
-        consider(false, nt, rows, s, n_rt, n_tt, rounds * each);
-      }
+    const int64_t n_tt = (M + nt - 1) / nt;
+    for (int s = 1; s <= kTcMaxSplit && s <= nkb; ++s) {
+      const int at_once = i8_clusters_at_once(s, sms);
+      const int64_t rounds = (n_rt * n_tt + at_once - 1) / at_once;
+      int64_t c = rounds * ((nkb + s - 1) / s) * i8_block_cost(nt, kRows + nt);
+      c = (c > hbm ? c : hbm) + rounds * (7500 + 16 * nt) + (s > 1 ? 1500 + 16 * nt : 0);
+      consider(false, nt, s, n_rt, n_tt, n_rt * n_tt, 1, c);
     }
   }
   return best;
@@ -204,24 +214,28 @@ static int launch_i8_split(const I8TcParams& p, const CUtensorMap& xmap, const C
                             dim3(kTcThreads), I8SplitCfg<NT>::SMEM, p.split, s, p, xmap, wmap);
 }
 
-static int launch_i8_pair(const I8TcParams& p, const CUtensorMap& xmap, const CUtensorMap& wmap,
-                          int sms, cudaStream_t s) {
+static int launch_i8_pair(const I8TcParams& p, const CUtensorMap& xmap, const CUtensorMap& xtail,
+                          const CUtensorMap& wmap, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> smem_set{0};
   if (!ensure_smem_limit(i8_pair_kernel, I8PairCfg::SMEM, smem_set)) return CQ_ERR_CUDA;
-  const int tiles = p.n_rt * p.n_tt, units = sms / 2;
+  const int tiles = p.main_tiles + (p.n_rt * p.n_tt - p.main_tiles) * p.cut, units = sms / 2;
   return launch_pdl_cluster(i8_pair_kernel, dim3(2u * (tiles < units ? tiles : units)),
-                            dim3(kTcThreads), I8PairCfg::SMEM, 2, s, p, xmap, wmap);
+                            dim3(kTcThreads), I8PairCfg::SMEM, 2, s, p, xmap, xtail, wmap);
 }
 
 static int i8_tc(const I8LinearParams& q, const I8TcPlan& g, const int8_t* xq,
                  const float* absmax, bool early_w, int sms, cudaStream_t s) {
-  CUtensorMap xmap, wmap;
+  CUtensorMap xmap, xtail, wmap;
   int st = encode_i8_rows(&xmap, xq, q.M, q.K, g.pair ? g.NT / 2 : g.NT);
   if (st != CQ_OK) return st;
+  if (g.pair) {
+    st = encode_i8_rows(&xtail, xq, q.M, q.K, g.NT / g.cut / 2);
+    if (st != CQ_OK) return st;
+  }
   const int64_t half = q.N / 2;
   const bool one_box = q.swiglu && half % 8 == 0;
-  st = !q.swiglu ? encode_i8_rows(&wmap, q.w, q.N, q.K, g.rows)
-                 : encode_i8_gate_up(&wmap, q.w, half, q.K, one_box ? g.rows / 16 : 0);
+  st = !q.swiglu ? encode_i8_rows(&wmap, q.w, q.N, q.K, kRows)
+                 : encode_i8_gate_up(&wmap, q.w, half, q.K, one_box ? kRows / 16 : 0);
   if (st != CQ_OK) return st;
   I8TcParams p = {};
   p.absmax = absmax;
@@ -235,12 +249,14 @@ static int i8_tc(const I8LinearParams& q, const I8TcPlan& g, const int8_t* xq,
   p.n_tt = g.n_tt;
   p.nkb = g.nkb;
   p.split = g.split;
-  p.rows = g.rows;
-  p.w_boxes = one_box ? 1 : g.rows / 16;
+  p.w_boxes = one_box ? 1 : kRows / 16;
   p.nt = g.NT;
+  p.main_tiles = g.main_tiles;
+  p.cut = g.cut;
+  p.tail_nt = g.NT / g.cut;
   p.early_w = early_w;
   p.timeout_ns = kDefaultTimeoutNs;
-  if (g.pair) return launch_i8_pair(p, xmap, wmap, sms, s);
+  if (g.pair) return launch_i8_pair(p, xmap, xtail, wmap, sms, s);
   switch (g.NT) {
     case 32: return launch_i8_split<32>(p, xmap, wmap, s);
     case 64: return launch_i8_split<64>(p, xmap, wmap, s);
@@ -274,7 +290,7 @@ static int i8_gemm_impl(const void* x, const float* absmax, int64_t M, const int
   if (i8_streams(M, K))
     return codes ? i8_linear<I8_SRC_CODES>(p, sms, s) : i8_linear<I8_SRC_BF16>(p, sms, s);
   const I8TcPlan g = i8_tc_plan(M, N, K, epilogue, sms);
-  if (static_cast<int64_t>(g.n_rt) * g.n_tt * g.split >= (int64_t)1 << 30)
+  if (static_cast<int64_t>(g.n_rt) * g.n_tt * g.split >= (int64_t)1 << 28)
     return CQ_ERR_UNSUPPORTED;
   const int8_t* xq = static_cast<const int8_t*>(x);
   if (!codes) {

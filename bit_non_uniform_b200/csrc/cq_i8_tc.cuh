@@ -5,9 +5,8 @@
 // shared memory, K-major with the 128-byte swizzle, loaded by TMA in blocks
 // of 128 bytes of K; the INT32 accumulators live in tensor memory.
 // Two kernels, chosen by a cost estimate on the host:
-//   * i8_split_kernel: one tile of up to 128 rows x NT tokens per cluster, K
-//     split over the cluster's CTAs (1 to 8).  The MMA always covers 128 rows;
-//     a tile of fewer loads fewer and ignores the others' sums.  For few tokens or few tiles: weights are
+//   * i8_split_kernel: one tile of 128 rows x NT tokens per cluster, K split
+//     over the cluster's CTAs (1 to 8).  For few tokens or few tiles: weights are
 //     read by all SMs although there are fewer tiles than SMs, and the INT32
 //     parts are summed through distributed shared memory, each CTA finishing
 //     its share of the columns.  (A first version split the K blocks of the
@@ -170,9 +169,10 @@ struct I8TcParams {
   int swiglu, out_bf16;
   int n_rt, n_tt, nkb;      // row tiles, token tiles, K blocks
   int split;                // CTAs per tile (i8_split_kernel)
-  int rows;                 // weight rows per CTA, a multiple of 16
-  int w_boxes;              // SwiGLU: boxes per block of K (1, or rows / 16)
-  int nt;                   // tokens per tile (i8_pair_kernel)
+  int w_boxes;              // SwiGLU: boxes per block of K (1, or 8)
+  // i8_pair_kernel: tokens per tile; the first `main_tiles` tiles are whole,
+  // each of the others is cut into `cut` parts of tail_nt tokens
+  int nt, main_tiles, cut, tail_nt;
   int early_w;              // the weights may be read before griddep_wait
   uint64_t timeout_ns;
 };
@@ -212,7 +212,7 @@ __device__ __forceinline__ I8Lane i8_lane(const I8TcParams& p, int rt0, int m0, 
   l.m0 = m0;
   l.mv = p.M - m0 < nt ? p.M - m0 : nt;
   l.col = rt0 + (p.swiglu ? (l.row >> 4) * 8 + (lane & 7) : l.row);
-  l.live = l.col < l.cols && l.row < p.rows;
+  l.live = l.col < l.cols;
   const int wrow = p.swiglu && (lane & 8) ? l.cols + l.col : l.col;
   l.ws = l.live ? __ldg(p.wscale + wrow) : 0.f;
   return l;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int tt = tile / p.n_rt, rt = tile - tt * p.n_rt;
   const int kb0 = static_cast<int>(static_cast<int64_t>(part) * p.nkb / S);
   const int kb1 = static_cast<int>(static_cast<int64_t>(part + 1) * p.nkb / S);
-  const int rt0 = rt * (p.swiglu ? p.rows / 2 : p.rows);
+  const int rt0 = rt * (p.swiglu ? kRows / 2 : kRows);
   const uint64_t tmo = p.timeout_ns;
 
   if (tid == 0) {
@@ -373,9 +373,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   I8Lane l = {};
   if (warp == kTcProducer) {
     if (lane == 0) {
-      const uint32_t bytes = static_cast<uint32_t>(p.rows + NT) * kTcBlock;
       auto load_w = [&](int kb, int st) {
-        mbar_arrive_expect_tx(bar_full + 8 * st, bytes);
+        mbar_arrive_expect_tx(bar_full + 8 * st, C::STAGE);
         i8_load_w<false>(p, base + st * C::STAGE, &wmap, kb * kTcBlock, rt0, bar_full + 8 * st);
       };
       // weights no preceding kernel writes are fetched while it ends
@@ -512,8 +511,32 @@ struct I8PairCfg {
   static_assert(SMEM <= 227 * 1024 && 2 * NT <= kTmemCols, "budgets");
 };
 
+// Tile t of the pair kernel.  The last tiles, which would keep only some of
+// the pairs busy, may be cut along their tokens: 4096 tokens of 6144 x 7168
+// are 384 tiles for 74 pairs, and uncut the sixth round keeps 14 pairs busy.
+struct I8Tile {
+  int rt, m0, nt;           // row tile, first token, tokens
+  bool tail;
+};
+__device__ __forceinline__ I8Tile i8_tile(const I8TcParams& p, int t) {
+  I8Tile i;
+  int part = 0, whole = t;
+  i.tail = t >= p.main_tiles;
+  if (i.tail) {
+    const int j = t - p.main_tiles;
+    whole = p.main_tiles + j / p.cut;
+    part = j % p.cut;
+  }
+  const int tt = whole / p.n_rt;
+  i.rt = whole - tt * p.n_rt;
+  i.nt = i.tail ? p.tail_nt : p.nt;
+  i.m0 = tt * p.nt + part * p.tail_nt;
+  return i;
+}
+
 __global__ void __launch_bounds__(kTcThreads, 1)
     i8_pair_kernel(const __grid_constant__ I8TcParams p, const __grid_constant__ CUtensorMap xmap,
+                   const __grid_constant__ CUtensorMap xtail,
                    const __grid_constant__ CUtensorMap wmap) {
   using C = I8PairCfg;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -535,7 +558,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int rank = static_cast<int>(cluster_rank());
   const int unit = static_cast<int>(blockIdx.x) >> 1;
   const int units = static_cast<int>(gridDim.x) >> 1;
-  const int NT = p.nt, half = NT / 2;
 
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -556,6 +578,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   if (warp == kTcProducer && lane == 0) {
     prefetch_tensormap(&xmap);
+    prefetch_tensormap(&xtail);
     prefetch_tensormap(&wmap);
   }
   __syncthreads();
@@ -566,21 +589,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
 
-  const int tiles = p.n_rt * p.n_tt;
+  const int tiles = p.main_tiles + (p.n_rt * p.n_tt - p.main_tiles) * p.cut;
   const uint64_t tmo = p.timeout_ns;
   const int cta_rows = p.swiglu ? 64 : kRows;               // output columns of this CTA's rows
 
   if (warp == kTcProducer) {
     if (lane == 0) {
       const uint32_t full0 = cluster_addr(bar_full, 0);
-      const uint32_t bytes = 2u * static_cast<uint32_t>(C::A_BYTES + half * kTcBlock);
       int st = 0, loads = 0;
       uint32_t round = 0;
       bool ok = true;
       for (int t = unit; ok && t < tiles; t += units) {
-        const int tt = t / p.n_rt, rt = t - tt * p.n_rt;
-        const int m0 = tt * NT + rank * half;
-        const int w0 = (rt * 2 + rank) * cta_rows;
+        const I8Tile tile = i8_tile(p, t);
+        const int half = tile.nt / 2, m0 = tile.m0 + rank * half;
+        const int w0 = (tile.rt * 2 + rank) * cta_rows;
+        const uint32_t bytes = 2u * static_cast<uint32_t>(C::A_BYTES + half * kTcBlock);
+        const CUtensorMap* const xm = tile.tail ? &xtail : &xmap;
         for (int kb = 0; kb < p.nkb; ++kb) {
           if (!wait_phase(bar_empty + 8 * st, (round & 1u) ^ 1u, abort_flag, tmo,
                           SITE_I8_EMPTY)) {
@@ -591,7 +615,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const uint32_t bar = full0 + 8 * st;
           if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * st, bytes);
           i8_load_w<true>(p, a, &wmap, kb * kTcBlock, w0, bar);
-          tma_load_2d_pair(a + C::A_BYTES, &xmap, kb * kTcBlock, m0, bar);
+          tma_load_2d_pair(a + C::A_BYTES, xm, kb * kTcBlock, m0, bar);
           ++loads;
           if (++st == C::STAGES) {
             st = 0;
@@ -620,11 +644,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncwarp();
   } else if (warp == kTcMma) {
     if (lane == 0 && rank == 0) {
-      const uint32_t idesc = idesc_s8_s32(2 * kRows, NT);
       int st = 0;
       uint32_t round = 0, done = 0;
       bool ok = true;
       for (int t = unit; ok && t < tiles; t += units) {
+        const uint32_t idesc = idesc_s8_s32(2 * kRows, i8_tile(p, t).nt);
         const uint32_t db = done & 1u;
         if (!wait_phase(bar_dfree + 8 * db, ((done >> 1) & 1u) ^ 1u, abort_flag, tmo,
                         SITE_I8_DFREE))
@@ -666,9 +690,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t dfree0 = cluster_addr(bar_dfree, 0);
     uint32_t done = 0;
     for (int t = unit; t < tiles; t += units) {
-      const int tt = t / p.n_rt, rt = t - tt * p.n_rt;
-      const I8Lane l = i8_lane(p, (rt * 2 + rank) * cta_rows, tt * NT, NT);
-      i8_load_scales(p, l.m0, l.mv, NT, s_sx);
+      const I8Tile tile = i8_tile(p, t);
+      const I8Lane l = i8_lane(p, (tile.rt * 2 + rank) * cta_rows, tile.m0, tile.nt);
+      i8_load_scales(p, l.m0, l.mv, tile.nt, s_sx);
       const uint32_t db = done & 1u;
       const bool ok = wait_phase(bar_dfull + 8 * db, (done >> 1) & 1u, abort_flag, tmo,
                                  SITE_I8_DFULL);
