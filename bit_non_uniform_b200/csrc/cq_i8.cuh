@@ -142,38 +142,48 @@ __device__ __forceinline__ void i8_stage_rows(const I8Rows& src, int cnt, int K,
   } else {
     if (threadIdx.x < kI8MaxTokens) s_max[threadIdx.x] = 0u;
     i8_sync();
-    // each row is shared by `parts` warps (short loops: a cold instruction
-    // cache costs a small call more than the second read of the row)
-    const int parts = cnt >= kI8Warps ? 1 : kI8Warps / cnt;
-    const int step = parts * 32, v0 = (warp % parts) * 32 + lane, nv = K / 8;
-    const int j0 = warp / parts, dj = kI8Warps / parts;
-    for (int j = j0; j < cnt; j += dj) {
-      const uint8_t* row = row_ptr(j);
+    // each row is shared by `parts` warps (cnt <= 16: a warp has one row at
+    // most); a thread keeps its first 8 values between the two passes and
+    // reads the others again (short loops: a cold instruction cache costs a
+    // small call more than that)
+    const int parts = kI8Warps / cnt, j = warp / parts;
+    const int step = parts * 32, v0 = (warp - j * parts) * 32 + lane, nv = K / 8;
+    const uint8_t* const row = j < cnt ? row_ptr(j) : nullptr;
+    float first[8];
+    if (row) {
       float mx = 0.f;
+      if (v0 < nv) {
+        i8_load8<SRC>(row, static_cast<int64_t>(v0) * 8, first);
 #pragma unroll 8
-      for (int v = v0; v < nv; v += step) {
-        float x[8];
-        i8_load8<SRC>(row, static_cast<int64_t>(v) * 8, x);
+        for (int v = v0 + step; v < nv; v += step) {
+          float x[8];
+          i8_load8<SRC>(row, static_cast<int64_t>(v) * 8, x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(x[i]));
+          for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(x[i]));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(first[i]));
       }
       const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
       if (lane == 0) atomicMax(&s_max[j], m);
     }
     i8_sync();
-    for (int j = j0; j < cnt; j += dj) {
-      const uint8_t* row = row_ptr(j);
+    if (row) {
       const float mx = __uint_as_float(s_max[j]);
       const float inv = mx > 0.f ? __fdiv_rn(127.0f, mx) : 0.f;
-#pragma unroll 4
-      for (int v = v0; v < nv; v += step) {
-        float x[8];
-        i8_load8<SRC>(row, static_cast<int64_t>(v) * 8, x);
+      auto put = [&](int v, const float (&x)[8]) {
         *reinterpret_cast<uint2*>(xs + j * stride + v * 8) =
             make_uint2(i8_code4(x[0], x[1], x[2], x[3], inv),
                        i8_code4(x[4], x[5], x[6], x[7], inv));
+      };
+      if (v0 < nv) put(v0, first);
+#pragma unroll 4
+      for (int v = v0 + step; v < nv; v += step) {
+        float x[8];
+        i8_load8<SRC>(row, static_cast<int64_t>(v) * 8, x);
+        put(v, x);
       }
-      if (lane == 0 && warp % parts == 0) s_scale[j] = __fdiv_rn(mx, 127.0f);
+      if (lane == 0 && v0 == 0) s_scale[j] = __fdiv_rn(mx, 127.0f);
     }
     i8_sync();
   }
@@ -653,9 +663,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   // caller's and were complete before the first began
   i8_plan(p, s);
   const int nc = s.n[1];
-  const int64_t W = static_cast<int64_t>(nc) * rows;
-  int64_t lo = W * blockIdx.x / gridDim.x;       // next row of the chunks' rows
-  const int64_t hi = W * (blockIdx.x + 1) / gridDim.x;
+  const int64_t W = static_cast<int64_t>(nc) * rows;         // below 2^27
+  int lo = static_cast<int>(W * blockIdx.x / gridDim.x);     // next row of the chunks' rows
+  const int hi = static_cast<int>(W * (blockIdx.x + 1) / gridDim.x);
 
   // the passes of this CTA: rows [a, a + nr) of a chunk, all with its routes
   struct Work {
@@ -663,7 +673,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     int64_t e;
   };
   auto next = [&](Work& w) {
-    const int ch = static_cast<int>(lo / rows);
+    const int ch = lo / rows;
     if (ch != w.ch) {
       // the chunk's expert: largest d with chunk[d] <= ch
       int d0 = 0, d1 = s.n[0];
@@ -678,9 +688,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       w.e = s.expert[d0];
     }
     const int per_pass = kI8AccBytes / (64 * w.cnt) * rpt;  // rows whose accumulators fit
-    w.a = static_cast<int>(lo - static_cast<int64_t>(ch) * rows);
+    w.a = lo - ch * rows;
     w.nr = rows - w.a < per_pass ? rows - w.a : per_pass;
-    if (hi - lo < w.nr) w.nr = static_cast<int>(hi - lo);
+    if (hi - lo < w.nr) w.nr = hi - lo;
     lo += w.nr;
   };
   auto pass_of = [&](const Work& w) {

@@ -29,6 +29,7 @@
 // and TMEM.
 #pragma once
 
+#include "cq_a8.cuh"
 #include "cq_i8.cuh"
 
 namespace cq {
