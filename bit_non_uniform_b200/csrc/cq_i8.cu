@@ -102,8 +102,10 @@ static int i8_clusters_at_once(int s, int sms) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, i8_split_kernel<128>, &cfg) != cudaSuccess || n <= 0)
+  if (cudaOccupancyMaxActiveClusters(&n, i8_split_kernel<128>, &cfg) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
     return sms / s;
+  }
   known[dev][s].store(n, std::memory_order_relaxed);
   return n;
 }

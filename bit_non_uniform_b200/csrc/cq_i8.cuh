@@ -150,6 +150,15 @@ __device__ __forceinline__ void i8_stage_rows(const I8Rows& src, int cnt, int K,
     const int step = parts * 32, v0 = (warp - j * parts) * 32 + lane, nv = K / 8;
     const uint8_t* const row = j < cnt ? row_ptr(j) : nullptr;
     float first[8];
+    // the largest magnitude: of a token's activations as cq_quant_rows takes
+    // it (NaN ignored); of computed values NaN counts as the largest, so that
+    // what overflowed upstream does not come out as zeros
+    auto larger = [](float m, float x) {
+      if constexpr (SRC == I8_SRC_F32)
+        return __uint_as_float(max(__float_as_uint(m), __float_as_uint(x) & 0x7FFFFFFFu));
+      else
+        return fmaxf(m, fabsf(x));
+    };
     if (row) {
       float mx = 0.f;
       if (v0 < nv) {
@@ -159,10 +168,10 @@ __device__ __forceinline__ void i8_stage_rows(const I8Rows& src, int cnt, int K,
           float x[8];
           i8_load8<SRC>(row, static_cast<int64_t>(v) * 8, x);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(x[i]));
+          for (int i = 0; i < 8; ++i) mx = larger(mx, x[i]);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(first[i]));
+        for (int i = 0; i < 8; ++i) mx = larger(mx, first[i]);
       }
       const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
       if (lane == 0) atomicMax(&s_max[j], m);

@@ -415,6 +415,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncwarp();
   } else if (warp == kTcMma) {
     if (lane == 0) {
+      griddep_wait();                       // the bounded waits start after it
       const uint32_t idesc = idesc_s8_s32(kRows, NT);
       int st = 0;
       uint32_t round = 0, acc = 0;

@@ -55,6 +55,22 @@ def libcq_compute(layer: torch.Tensor, E_local: int, H: int, I: int, G: int,
     return run
 
 
+def libcq_i8_compute(w_gu: torch.Tensor, s_gu: torch.Tensor, w_dn: torch.Tensor,
+                     s_dn: torch.Tensor) -> Compute:
+    """The rank's expert computation on the GPU for a layer kept in INT8:
+    cq_moe_i8 over its experts (w_gu int8 [E_local][2I][H], s_gu [E_local][2I],
+    w_dn int8 [E_local][H][I], s_dn [E_local][H]), combined per row.  Meant for
+    the few rows of a decode step."""
+    from . import F32, cq_moe_i8
+
+    def run(tokens: torch.Tensor, ids: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
+        _, out = cq_moe_i8(tokens, ids, w, w_gu, s_gu, w_dn, s_dn, out_dtype=F32,
+                           route_out=False)
+        return out
+
+    return run
+
+
 def _a2a(out: torch.Tensor, inp: torch.Tensor, out_splits, in_splits, group) -> None:
     dist.all_to_all_single(out, inp, list(out_splits), list(in_splits), group=group)
 

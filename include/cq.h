@@ -364,6 +364,7 @@ CQ_API int cq_linear_i8(const uint16_t *x, int64_t M, const int8_t *wq, const fl
  *   out       [T][H] in out_dtype (may be NULL)
  *   workspace device scratch of cq_moe_i8_workspace_size(...) bytes, 256-byte
  *             aligned
+ * An activation that makes h overflow or NaN makes its route's y_r not finite.
  * A shared expert of the same width is one more expert: id E-1 and weight 1
  * in an extra column of topk_ids.  H and I multiples of 16, at most 131072;
  * k at most 1024; E at most 16384.  More than 1024 routes run as successive

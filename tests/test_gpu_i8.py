@@ -289,6 +289,27 @@ def test_moe_all_routes_dropped(cq):
     assert bool((out[0] == 0).all()) and bool((out[2] == 0).all())
 
 
+@pytest.mark.parametrize("T", [2, 12])
+def test_moe_infinite_token_and_overflow_are_not_hidden(cq, T):
+    """An infinite activation, or gate and up values whose product overflows
+    FP32, leave outputs that are not finite; other tokens keep their bits."""
+    g = gen(13)
+    k, E, H, I = 2, 4, 512, 64
+    x, lw = tokens(g, T, H), layer(g, E, H, I)
+    ids, w = distinct_ids(g, T, E, k), torch.ones(T, k, device="cuda")
+    clean = cq.cq_moe_i8(x, ids, w, *lw)[0]
+    bad = x.clone()
+    bad[1, 7] = float("inf")
+    ro, out = cq.cq_moe_i8(bad, ids, w, *lw)
+    assert not bool(torch.isfinite(ro[k:2 * k]).any()) and not bool(torch.isfinite(out[1]).any())
+    assert torch.equal(ro[:k], clean[:k]) and torch.equal(ro[2 * k:], clean[2 * k:])
+    bad = x.clone()
+    bad[1] = (x[1].float() * 1e30).to(torch.bfloat16)          # g and u near 1e30
+    ro, out = cq.cq_moe_i8(bad, ids, w, *lw)
+    assert not bool(torch.isfinite(ro[k:2 * k]).any())
+    assert torch.equal(ro[:k], clean[:k])
+
+
 def test_moe_the_same_expert_twice(cq):
     g = gen(9)
     T, k, E, H, I = 12, 3, 4, 256, 96
@@ -606,5 +627,28 @@ def test_binding_refuses_mismatched_tensors(cq):
                  (x, ids, w, lw[0][:, :60], *lw[1:])):
         with pytest.raises(ValueError):
             cq.cq_moe_i8(*args)
+    small = torch.zeros(256, dtype=torch.uint8, device="cuda")
     with pytest.raises(cq.CQError):
-        cq.cq_moe_i8(x, ids, w, *lw, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+        cq.cq_moe_i8(x, ids, w, *lw, workspace=small)
+    xm = tokens(g, 100, 64)
+    with pytest.raises(cq.CQError):
+        cq.cq_linear_i8(xm, wq, ws, workspace=small)
+    with pytest.raises(cq.CQError):                  # not 256-byte aligned
+        cq.cq_linear_i8(xm, wq, ws,
+                        workspace=torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")[16:])
+    with pytest.raises(ValueError):
+        cq.cq_linear_i8(xm, wq, ws, workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+
+
+def test_expert_parallel_layer_on_one_rank(cq):
+    """The expert-parallel exchange around INT8 experts: on one rank the bits
+    of the layer itself."""
+    from bit_non_uniform_b200.ep import MoeExpertParallel, libcq_i8_compute
+    g = gen(80)
+    T, k, E, H, I = 6, 3, 8, 512, 96
+    x, lw = tokens(g, T, H), layer(g, E, H, I)
+    ids, w = distinct_ids(g, T, E, k), torch.rand(T, k, generator=g, device="cuda")
+    ids[2] = -1                                      # a token without routes
+    want = cq.cq_moe_i8(x, ids, w, *lw)[1]
+    ep = MoeExpertParallel(E, H, libcq_i8_compute(*lw))
+    assert torch.equal(ep.forward(x, ids, w), want)
