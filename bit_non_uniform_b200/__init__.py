@@ -375,12 +375,8 @@ def _on_device(index: int, stream):
     return stack
 
 
-def _elsewhere(index: int, stream) -> bool:
-    return stream is not None or index != torch._C._cuda_getDevice()
-
-
-def _raw_stream(index: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(index)
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream      # of a device's current stream
 
 
 def _tensor(name, t, dtype, shape, index: int) -> int:
@@ -427,17 +423,19 @@ def gemm_i8_workspace(M, N, K, epilogue=EPI_NONE, device="cuda"):
 
 
 def _i8_product(where, x, absmax, wq, wscale, epilogue, out_dtype, out, workspace, stream):
-    if x.dim() != 2 or wq.dim() != 2:
-        raise ValueError(f"{where}: activations [M][K] and weights [N][K] expected")
-    _need_cuda(x)
+    try:
+        M, K = x.shape
+        N, _ = wq.shape
+    except ValueError:
+        raise ValueError(f"{where}: activations [M][K] and weights [N][K] expected") from None
     index = x.get_device()
-    if _elsewhere(index, stream):
+    if index < 0:
+        _need_cuda(x)
+    if stream is not None or index != _current_device():
         with _on_device(index, stream):
             return _i8_product(where, x, absmax, wq, wscale, epilogue, out_dtype, out, workspace,
                                None)
-    L = lib()
-    M, K = x.shape
-    N = wq.shape[0]
+    L = _lib or lib()
     dt = _out_dtype(out_dtype)
     px = _tensor("x", x, torch.bfloat16 if absmax is None else torch.int8, (M, K), index)
     pw = _tensor("wq", wq, torch.int8, (N, K), index)
@@ -494,19 +492,21 @@ def cq_moe_i8(tokens, topk_ids, topk_w, w_gu, s_gu, w_dn, s_dn, out_dtype: int =
     """Routed-expert FFN of one MoE layer on INT8 experts, for a few tokens:
     w_gu int8 [E][2I][H], s_gu [E][2I], w_dn int8 [E][H][I], s_dn [E][H].
     Returns (route_out, out) as cq_moe_grouped_gemm does."""
-    if tokens.dim() != 2 or topk_ids.dim() != 2 or w_gu.dim() != 3 or w_dn.dim() != 3:
+    try:
+        T, H = tokens.shape
+        _, k = topk_ids.shape
+        E, _, I = w_dn.shape
+    except ValueError:
         raise ValueError("cq_moe_i8: tokens [T][H], topk_ids [T][k], w_gu [E][2I][H] and "
-                         "w_dn [E][H][I] expected")
-    _need_cuda(tokens)
+                         "w_dn [E][H][I] expected") from None
     index = tokens.get_device()
-    if _elsewhere(index, stream):
+    if index < 0:
+        _need_cuda(tokens)
+    if stream is not None or index != _current_device():
         with _on_device(index, stream):
             return cq_moe_i8(tokens, topk_ids, topk_w, w_gu, s_gu, w_dn, s_dn, out_dtype,
                              route_out, combine, workspace)
-    L = lib()
-    T, H = tokens.shape
-    k = topk_ids.shape[1]
-    E, _, I = w_dn.shape
+    L = _lib or lib()
     dt = _out_dtype(out_dtype)
     pt = _tensor("tokens", tokens, torch.bfloat16, (T, H), index)
     pi = _tensor("topk_ids", topk_ids, torch.int32, (T, k), index)
@@ -541,25 +541,28 @@ def cq_moe_route(logits, k: int, bias=None, scoring: int = SCORE_SOFTMAX, renorm
                  scale: float = 1.0, stream=None):
     """The k experts of each row of router logits [T][E] (float32 or bfloat16):
     (topk_ids int32 [T][k], topk_w float32 [T][k]), as the MoE layers take them."""
-    if logits.dim() != 2:
-        raise ValueError("cq_moe_route: logits [T][E] expected")
-    _need_cuda(logits)
+    try:
+        T, E = logits.shape
+    except ValueError:
+        raise ValueError("cq_moe_route: logits [T][E] expected") from None
     dt = logits.dtype
     if dt is not torch.float32 and dt is not torch.bfloat16:
         raise ValueError(f"logits are {dt}, expected float32 or bfloat16")
     index = logits.get_device()
-    if _elsewhere(index, stream):
+    if index < 0:
+        _need_cuda(logits)
+    if stream is not None or index != _current_device():
         with _on_device(index, stream):
             return cq_moe_route(logits, k, bias, scoring, renorm, scale)
-    T, E = logits.shape
+    L = _lib or lib()
     pl = _tensor("logits", logits, dt, (T, E), index)
     pb = None if bias is None else _tensor("bias", bias, torch.float32, (E,), index)
     shape = (T, max(k, 0))
     ids = logits.new_empty(shape, dtype=torch.int32)
     w = logits.new_empty(shape, dtype=torch.float32)
-    _check(lib().cq_moe_route(pl, F32 if dt is torch.float32 else BF16, T, E, k, pb, scoring,
-                              1 if renorm else 0, scale, ids.data_ptr(), w.data_ptr(),
-                              _raw_stream(index)), "cq_moe_route")
+    _check(L.cq_moe_route(pl, F32 if dt is torch.float32 else BF16, T, E, k, pb, scoring,
+                          1 if renorm else 0, scale, ids.data_ptr(), w.data_ptr(),
+                          _raw_stream(index)), "cq_moe_route")
     return ids, w
 
 
