@@ -362,9 +362,23 @@ def cq_moe_grouped_gemm(tokens, topk_ids, topk_w, layer, E: int, H: int, I: int,
 # INT8 weights
 # ---------------------------------------------------------------------------
 # A decode step makes many of these calls, each a few microseconds long on the
-# GPU, so the host side of a call is kept short: one test per tensor, the
-# current stream's handle without a Stream object, and no context manager
-# where the call's device and stream are the current ones already.
+# GPU, so the host side of a call is kept short.  The plain call (everything on
+# the current device and stream, nothing to say about the arguments) is made by
+# the compiled module, in about half the time; all others go through Python:
+# one test per tensor, the current stream's handle without a Stream object, and
+# no context manager where device and stream are the current ones already.
+try:
+    from . import _cq_torch as _direct
+except ImportError:                        # not built (yet)
+    _direct = None
+
+
+def _direct_result(r, where):
+    if type(r) is int:
+        raise CQError(r, where)
+    return r
+
+
 def _on_device(index: int, stream):
     """The call's device and stream as the current ones (libcq launches on the
     current device)."""
@@ -466,6 +480,10 @@ def cq_gemm_i8(xq, absmax, wq, wscale, epilogue: int = EPI_NONE, out_dtype: int 
     weights [N][K] with one scale per output channel."""
     if absmax is None:
         raise ValueError("cq_gemm_i8 needs absmax (cq_quant_rows returns it)")
+    if _direct is not None and out is None and stream is None:
+        r = _direct.product(xq, absmax, wq, wscale, epilogue, out_dtype, workspace)
+        if r is not None:
+            return _direct_result(r, "cq_gemm_i8")
     return _i8_product("cq_gemm_i8", xq, absmax, wq, wscale, epilogue, out_dtype, out, workspace,
                        stream)
 
@@ -473,6 +491,10 @@ def cq_gemm_i8(xq, absmax, wq, wscale, epilogue: int = EPI_NONE, out_dtype: int 
 def cq_linear_i8(x, wq, wscale, epilogue: int = EPI_NONE, out_dtype: int = F32, out=None,
                  workspace=None, stream=None):
     """cq_gemm_i8 on bfloat16 activations, quantized per row inside the call."""
+    if _direct is not None and out is None and stream is None:
+        r = _direct.product(x, None, wq, wscale, epilogue, out_dtype, workspace)
+        if r is not None:
+            return _direct_result(r, "cq_linear_i8")
     return _i8_product("cq_linear_i8", x, None, wq, wscale, epilogue, out_dtype, out, workspace,
                        stream)
 
@@ -492,6 +514,11 @@ def cq_moe_i8(tokens, topk_ids, topk_w, w_gu, s_gu, w_dn, s_dn, out_dtype: int =
     """Routed-expert FFN of one MoE layer on INT8 experts, for a few tokens:
     w_gu int8 [E][2I][H], s_gu [E][2I], w_dn int8 [E][H][I], s_dn [E][H].
     Returns (route_out, out) as cq_moe_grouped_gemm does."""
+    if _direct is not None and combine and stream is None and (route_out is False
+                                                               or route_out is None):
+        r = _direct.moe(tokens, topk_ids, topk_w, w_gu, s_gu, w_dn, s_dn, out_dtype, workspace)
+        if r is not None:
+            return None, _direct_result(r, "cq_moe_i8")
     try:
         T, H = tokens.shape
         _, k = topk_ids.shape
@@ -541,6 +568,10 @@ def cq_moe_route(logits, k: int, bias=None, scoring: int = SCORE_SOFTMAX, renorm
                  scale: float = 1.0, stream=None):
     """The k experts of each row of router logits [T][E] (float32 or bfloat16):
     (topk_ids int32 [T][k], topk_w float32 [T][k]), as the MoE layers take them."""
+    if _direct is not None and stream is None:
+        r = _direct.route(logits, k, bias, scoring, renorm, scale)
+        if r is not None:
+            return _direct_result(r, "cq_moe_route")
     try:
         T, E = logits.shape
     except ValueError:

@@ -1,4 +1,5 @@
-"""Build libcq.so (the CUDA library) in-tree with nvcc for sm_100a.
+"""Build libcq.so (the CUDA library) in-tree with nvcc for sm_100a, and
+_cq_torch.so (its INT8 calls on torch tensors, host code) with g++.
 
     python -m bit_non_uniform_b200.build
 """
@@ -26,6 +27,35 @@ FLAGS = [
 ]
 
 
+TORCH_SRC = os.path.join(CSRC, "cq_torch.cpp")
+TORCH_LIB = os.path.join(HERE, "_cq_torch.so")
+CXX = os.environ.get("CXX", "g++")
+
+
+def build_torch(force: bool = False) -> str:
+    """The extension links against libcq.so beside it."""
+    if not force and os.path.exists(TORCH_LIB):
+        t = os.path.getmtime(TORCH_LIB)
+        if all(os.path.getmtime(d) <= t for d in (TORCH_SRC, os.path.join(INCLUDE, "cq.h"))):
+            return TORCH_LIB
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = TORCH_LIB + f".tmp{os.getpid()}"
+    subprocess.check_call([
+        CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"),
+        "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+        "-I", os.path.join(cuda, "include"), TORCH_SRC, "-o", tmp,
+        "-L", HERE, "-l:libcq.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(root, "lib"),
+        "-ltorch_python", "-ltorch", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+    os.replace(tmp, TORCH_LIB)
+    return TORCH_LIB
+
+
 def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
@@ -37,6 +67,7 @@ def _stale() -> bool:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
+        build_torch()
         return LIB
     objs = []
     build_dir = os.path.join(HERE, "_build")
@@ -52,6 +83,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     subprocess.check_call([NVCC, "-shared", "-gencode", "arch=compute_100a,code=sm_100a",
                            *objs, "-o", tmp, "-lcuda"])
     os.replace(tmp, LIB)
+    build_torch(force)
     return LIB
 
 

@@ -127,3 +127,22 @@ def test_binding_refuses_cpu_tensors(cq):
         cq.cq_moe_i8(x, torch.zeros((2, 1), dtype=torch.int32), torch.ones((2, 1)),
                      torch.zeros((1, 32, 64), dtype=torch.int8), torch.ones((1, 32)),
                      torch.zeros((1, 64, 16), dtype=torch.int8), torch.ones((1, 64)))
+
+
+def test_compiled_calls_leave_everything_unusual_to_the_binding(cq):
+    """The compiled module is built beside libcq and answers None (the general
+    path then says what is wrong) for tensors it does not take."""
+    from bit_non_uniform_b200 import _cq_torch as direct
+    x = torch.zeros((2, 64), dtype=torch.bfloat16)
+    w, s = torch.zeros((8, 64), dtype=torch.int8), torch.ones(8)
+    ids, tw = torch.zeros((2, 1), dtype=torch.int32), torch.ones((2, 1))
+    lw = (torch.zeros((1, 32, 64), dtype=torch.int8), torch.ones((1, 32)),
+          torch.zeros((1, 64, 16), dtype=torch.int8), torch.ones((1, 64)))
+    for args in ((x, None, w, s, 0, 0, None), (1, None, w, s, 0, 0, None), (), (x,),
+                 (x, None, None, None, 0, 0, None), (x[0], None, w, s, 0, 0, None),
+                 (x, None, w, s, "0", 1 << 80, None)):
+        assert direct.product(*args) is None, args
+    for args in ((x, ids, tw, *lw, 0, None), (x, ids, None, *lw, 0, None), (x, 3), ()):
+        assert direct.moe(*args) is None, args
+    for args in ((tw, 1, None, 0, True, 1.0), (None, 1, None, 0, True, 1.0), (tw,)):
+        assert direct.route(*args) is None, args

@@ -652,3 +652,33 @@ def test_expert_parallel_layer_on_one_rank(cq):
     want = cq.cq_moe_i8(x, ids, w, *lw)[1]
     ep = MoeExpertParallel(E, H, libcq_i8_compute(*lw))
     assert torch.equal(ep.forward(x, ids, w), want)
+
+
+def test_compiled_and_general_calls_agree(cq, monkeypatch):
+    g = gen(90)
+    H, I, E, k = 256, 96, 6, 2
+    lw = layer(g, E, H, I)
+    wq, ws = codes(g, 300, H), scales(g, 300, K=H)
+    bias = torch.randn(E, generator=g, device="cuda")
+
+    def calls(T):
+        gg = gen(T)
+        x = tokens(gg, T, H)
+        xq, am = cq.cq_quant_rows(x)
+        logits = torch.randn(T, E, generator=gg, device="cuda")
+        ids, w = cq.cq_moe_route(logits, k, bias=bias, scale=1.5)
+        bufs = (cq.gemm_i8_workspace(T, 300, H), cq.moe_i8_workspace(T, k, E, H, I))
+        return (ids, w, cq.cq_linear_i8(x, wq, ws, epilogue=cq.EPI_SWIGLU),
+                cq.cq_linear_i8(x, wq, ws, out_dtype=cq.BF16, workspace=bufs[0]),
+                cq.cq_gemm_i8(xq, am, wq, ws),
+                cq.cq_moe_i8(x, ids, w, *lw, route_out=False)[1],
+                cq.cq_moe_i8(x, ids, w, *lw, out_dtype=cq.BF16, route_out=None,
+                             workspace=bufs[1])[1])
+
+    assert cq._direct is not None
+    for T in (0, 1, 5, 70):
+        fast = calls(T)
+        with monkeypatch.context() as m:
+            m.setattr(cq, "_direct", None)
+            for a, b in zip(fast, calls(T)):
+                assert a.dtype == b.dtype and a.shape == b.shape and torch.equal(a, b)
