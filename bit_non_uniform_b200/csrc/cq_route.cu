@@ -44,7 +44,7 @@ extern "C" CQ_API int cq_moe_route(const void* logits, int logits_dtype, int64_t
   p.renorm = renorm;
   p.bf16 = logits_dtype == CQ_DTYPE_BF16;
   p.scale = scale;
-  p.vec4 = E % 4 == 0 && aligned(logits, p.bf16 ? 8 : 16) && (!bias || aligned(bias, 16));
+  p.vec4 = E % 4 == 0 && aligned(logits, p.bf16 ? 8 : 16);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // NV values in each of 32 lanes (a multiple of 4: whole vectors)
   if (E <= 128) return launch_route<4>(p, s);

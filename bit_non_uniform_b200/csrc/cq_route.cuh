@@ -92,19 +92,20 @@ __device__ __forceinline__ float warp_sort_desc(float v) {
   return v;
 }
 
-// NV values per lane.  The lane's value i is expert ((i / 4) 32 + lane) 4 + i % 4
+// NV values per lane, a multiple of 4.  The lane's value i is expert ((i / 4) 32 + lane) 4 + i % 4
 // where rows and bias can be read in fours (vec4), else i 32 + lane.
 template <int NV>
 __global__ void __launch_bounds__(kRtWarps * 32)
     route_topk_kernel(const __grid_constant__ RouteParams p) {
   __shared__ RouteSmem smem[kRtWarps];
+  __shared__ float4 s_bias[NV * 8];      // zeros past E
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   RouteSmem& s = smem[warp];
   const float NEG = -INFINITY;
   griddep_wait();
   griddep_launch_dependents();
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRtWarps + warp;
-  if (t >= p.T) return;
+  const bool live = t < p.T;
   const int64_t base = t * p.E;
   auto expert = [&](int i) {
     return p.vec4 ? ((i >> 2) * 32 + lane) * 4 + (i & 3) : i * 32 + lane;
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kRtWarps * 32)
     for (int i = 0; i < NV; i += 4) {
       const int e = expert(i);
       float4 v = make_float4(NEG, NEG, NEG, NEG);
-      if (e < p.E) {
+      if (live && e < p.E) {
         if (p.bf16) {
           const uint2 q =
               __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.logits) + base +
@@ -138,9 +139,21 @@ __global__ void __launch_bounds__(kRtWarps * 32)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = i * 32 + lane;
-      key[i] = e < p.E ? route_logit(p, base + e) : NEG;
+      key[i] = live && e < p.E ? route_logit(p, base + e) : NEG;
     }
   }
+  // the CTA's bias, on its way together with the logits (read where it is
+  // used, it cost one token 2 us)
+  float* const bias = reinterpret_cast<float*>(s_bias);
+  if (p.bias) {
+#pragma unroll
+    for (int i = 0; i < NV / kRtWarps; ++i) {
+      const int e = i * kRtWarps * 32 + threadIdx.x;
+      bias[e] = e < p.E ? __ldg(p.bias + e) : 0.f;
+    }
+  }
+  __syncthreads();
+  if (!live) return;
   float top = NEG;
   double sum = 0.0;                      // softmax: sum of exp(l - top)
   if (!p.sigmoid) {
@@ -151,10 +164,19 @@ __global__ void __launch_bounds__(kRtWarps * 32)
     if (p.bias) {
       // picks compare p + bias: the sum in FP64 (the logits read again, so
       // that the loop stays rolled)
-#pragma unroll 1
-      for (int e = lane; e < p.E; e += 32) {
-        const float v = route_logit(p, base + e);
-        if (v > NEG) sum += route_exp64(v, top);
+      if (top > NEG) {
+        for (int e = lane; e < p.E; e += 128) {
+          double x[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float v = e + 32 * j < p.E ? route_logit(p, base + e + 32 * j) : NEG;
+            // (equal infinities count as 1)
+            x[j] = v == top ? 0.0 : static_cast<double>(v) - static_cast<double>(top);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = exp(x[j]);
+          sum += (x[0] + x[1]) + (x[2] + x[3]);
+        }
       }
       sum = warp_sum_f64(sum);
     } else if (!p.renorm) {
@@ -177,19 +199,14 @@ __global__ void __launch_bounds__(kRtWarps * 32)
     for (int i = 0; i < NV; i += 4) {
       float b[4];
       if (p.vec4) {
-        const int e = expert(i);
-        const float4 q = e < p.E ? __ldg(reinterpret_cast<const float4*>(p.bias + e))
-                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 q = s_bias[expert(i) >> 2];
         b[0] = q.x;
         b[1] = q.y;
         b[2] = q.z;
         b[3] = q.w;
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int e = expert(i + j);
-          b[j] = e < p.E ? __ldg(p.bias + e) : 0.f;
-        }
+        for (int j = 0; j < 4; ++j) b[j] = bias[expert(i + j)];
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -235,7 +252,7 @@ __global__ void __launch_bounds__(kRtWarps * 32)
       const float v = route_logit(p, base + e);
       const double sc = score64(v);
       s.score[c] = sc;
-      s.pick[c] = p.bias ? sc + static_cast<double>(__ldg(p.bias + e)) : static_cast<double>(v);
+      s.pick[c] = p.bias ? sc + static_cast<double>(bias[e]) : static_cast<double>(v);
     }
     __syncwarp();
     for (int c = lane; c < n; c += 32) {
@@ -261,7 +278,7 @@ __global__ void __launch_bounds__(kRtWarps * 32)
       for (uint32_t m = mask; m; m &= m - 1) {
         const int i = __ffs(m) - 1, e = expert(i);
         const float v = route_logit(p, base + e);
-        const double pick = p.bias ? score64(v) + static_cast<double>(__ldg(p.bias + e))
+        const double pick = p.bias ? score64(v) + static_cast<double>(bias[e])
                                    : static_cast<double>(v);
         if (pick > wp || (pick == wp && e < we)) {
           wp = pick;
