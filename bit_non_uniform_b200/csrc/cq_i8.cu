@@ -75,10 +75,10 @@ struct I8TcPlan {
 
 static size_t i8_round256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Products streamed from memory: up to 8 tokens (one block of MMA columns;
-// 6144 x 7168 with SwiGLU takes 12 us at 8 tokens and 13.5 on the tensor
-// cores, which take 16 in the same time), as long as their rows fit beside
-// the ring.
+// Products streamed from memory: up to 8 tokens, one block of MMA columns, as
+// long as their rows fit beside the ring.  6144 x 7168 with SwiGLU takes 10.3
+// us at 2 tokens and 12.1 at 8; on the tensor cores 12.5 at 16, and 3 us more
+// for rows that have to be quantized first.
 static bool i8_streams(int64_t M, int64_t K) { return M <= 8 && M <= i8_tokens_per_pass(K, 0); }
 
 // Clusters of `s` CTAs of the split kernel that run at once (a GPC's SMs need
@@ -370,7 +370,8 @@ using namespace cq;
 extern "C" CQ_API size_t cq_gemm_i8_workspace_size(int64_t M, int64_t N, int64_t K, int epilogue) {
   if (validate_i8(M, N, K, epilogue, CQ_DTYPE_F32) != CQ_OK || M == 0 || N == 0 || i8_streams(M, K))
     return 0;
-  return i8_round256(static_cast<size_t>(M) * K) + i8_round256(static_cast<size_t>(M) * sizeof(float));
+  return i8_round256(static_cast<size_t>(M) * K) +
+         i8_round256(static_cast<size_t>(M) * sizeof(float));
 }
 
 extern "C" CQ_API int cq_gemm_i8(const int8_t* xq, const float* absmax, int64_t M,

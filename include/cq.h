@@ -346,7 +346,8 @@ CQ_API int cq_linear_i8(const uint16_t *x, int64_t M, const int8_t *wq, const fl
 /*
  * cq_moe_i8 -- the routed-expert FFN of one MoE layer with INT8 experts, for
  * a few tokens (a decode step): two kernels that read each expert in use
- * once, and one that sums each token's routes.  For every route r = t*k + j with e = topk_ids[t][j]:
+ * once (again for every further 8 to 16 routes of one expert), and one that
+ * sums each token's routes.  For every route r = t*k + j with e = topk_ids[t][j]:
  *   xq, absmax = cq_quant_rows(tokens[t]);
  *   g|u   = RN(absmax / 127) * s_gu[e][n] * (xq . w_gu[e][n])
  *   h     = RN32(silu(g) * u), evaluated in FP64 so that the codes of
