@@ -545,7 +545,7 @@ __device__ __forceinline__ int warp_inclusive_sum(int v) {
 __device__ __forceinline__ void i8_plan_small(const I8MoeParams& p, const I8Plan& s) {
   const int lane = threadIdx.x;
   if (lane < 32) {
-    int id = lane < p.R ? __ldg(p.ids + lane) : -1;
+    int id = lane < p.R ? p.ids[lane] : -1;
     if (id < 0 || id >= p.E) id = -1;
     const unsigned same = __match_any_sync(0xffffffffu, id);
     const unsigned below = (1u << lane) - 1u;
@@ -584,7 +584,7 @@ __device__ __forceinline__ void i8_plan(const I8MoeParams& p, const I8Plan& s) {
   for (int i = tid; i < words; i += kI8Threads) s.bits[i] = 0u;
   __syncthreads();
   for (int r = tid; r < i8_plan_routes(p.R); r += kI8Threads) {
-    int id = r < p.R ? __ldg(p.ids + r) : -1;
+    int id = r < p.R ? p.ids[r] : -1;
     if (id < 0 || id >= p.E) id = -1;
     s.dense[r] = static_cast<int16_t>(id);
     if (id >= 0) atomicOr(&s.bits[id >> 5], 1u << (id & 31));
@@ -813,9 +813,9 @@ __global__ void __launch_bounds__(kI8CombineThreads)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int r = t * p.k + j0 + j;
-      const int id = j0 + j < p.k ? __ldg(p.ids + r) : -1;
+      const int id = j0 + j < p.k ? p.ids[r] : -1;
       const bool live = id >= 0 && id < p.E;
-      wj[j] = live ? __ldg(p.topk_w + r) : 0.f;
+      wj[j] = live ? p.topk_w[r] : 0.f;
       q[j] = live ? __ldcg(y + static_cast<int64_t>(j0 + j) * V) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll

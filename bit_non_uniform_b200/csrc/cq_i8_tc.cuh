@@ -217,7 +217,7 @@ __device__ __forceinline__ I8Lane i8_lane(const I8TcParams& p, int rt0, int m0, 
   l.col = rt0 + (p.swiglu ? (l.row >> 4) * 8 + (lane & 7) : l.row);
   l.live = l.col < l.cols;
   const int wrow = p.swiglu && (lane & 8) ? l.cols + l.col : l.col;
-  l.ws = l.live ? __ldg(p.wscale + wrow) : 0.f;
+  l.ws = l.live ? p.wscale[wrow] : 0.f;
   return l;
 }
 
@@ -282,7 +282,7 @@ __device__ __forceinline__ void i8_finish(const I8TcParams& p, const I8Lane& l, 
 __device__ __forceinline__ void i8_load_scales(const I8TcParams& p, int m0, int mv, int nt,
                                                float* s_sx) {
   for (int c = threadIdx.x; c < nt; c += kTcEpilogue)
-    s_sx[c] = c < mv ? __fdiv_rn(__ldg(p.absmax + m0 + c), 127.0f) : 0.f;
+    s_sx[c] = c < mv ? __fdiv_rn(p.absmax[m0 + c], 127.0f) : 0.f;
 }
 
 // Load this CTA's weight rows of one block of K.  SwiGLU: the tensor map's
@@ -734,8 +734,7 @@ constexpr int kQvThreads = 128;
 constexpr int kQvKeep = 8;                 // 16-byte loads kept per thread
 
 __global__ void __launch_bounds__(kQvThreads)
-    quant_rows_vec_kernel(const uint16_t* __restrict__ x, int M, int K, int8_t* __restrict__ xq,
-                          float* __restrict__ absmax) {
+    quant_rows_vec_kernel(const uint16_t* x, int M, int K, int8_t* xq, float* absmax) {
   __shared__ uint32_t red[kQvThreads / 32];
   griddep_wait();
   griddep_launch_dependents();

@@ -56,11 +56,36 @@ __device__ __forceinline__ double route_exp64(float l, float top) {
   return l == top ? 1.0 : exp(static_cast<double>(l) - static_cast<double>(top));
 }
 
+// Plain global loads (not the read-only path: a preceding kernel may still be
+// writing the data when this one starts), kept behind griddep_wait.
+__device__ __forceinline__ uint32_t route_ld16(const void* at) {
+  uint16_t v;
+  asm volatile("ld.global.b16 %0, [%1];" : "=h"(v) : "l"(at));
+  return v;
+}
+__device__ __forceinline__ float route_ld32(const void* at) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 route_ld64(const void* at) {
+  uint2 v;
+  asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(at));
+  return v;
+}
+__device__ __forceinline__ float4 route_ld128(const void* at) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(at));
+  return v;
+}
+
 // One logit, NaN as -inf.
 __device__ __forceinline__ float route_logit(const RouteParams& p, int64_t at) {
-  const float v = p.bf16 ? __uint_as_float(static_cast<uint32_t>(__ldg(
-                               static_cast<const uint16_t*>(p.logits) + at)) << 16)
-                         : __ldg(static_cast<const float*>(p.logits) + at);
+  const float v =
+      p.bf16 ? __uint_as_float(route_ld16(static_cast<const uint16_t*>(p.logits) + at) << 16)
+             : route_ld32(static_cast<const float*>(p.logits) + at);
   return fmaxf(v, -INFINITY);
 }
 
@@ -118,14 +143,11 @@ __global__ void __launch_bounds__(kRtWarps * 32)
       float4 v = make_float4(NEG, NEG, NEG, NEG);
       if (live && e < p.E) {
         if (p.bf16) {
-          const uint2 q =
-              __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.logits) + base +
-                                                   e));
+          const uint2 q = route_ld64(static_cast<const uint16_t*>(p.logits) + base + e);
           v = make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xFFFF0000u),
                           __uint_as_float(q.y << 16), __uint_as_float(q.y & 0xFFFF0000u));
         } else {
-          v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.logits) + base +
-                                                    e));
+          v = route_ld128(static_cast<const float*>(p.logits) + base + e);
         }
       }
       key[i] = v.x;
@@ -149,7 +171,7 @@ __global__ void __launch_bounds__(kRtWarps * 32)
 #pragma unroll
     for (int i = 0; i < NV / kRtWarps; ++i) {
       const int e = i * kRtWarps * 32 + threadIdx.x;
-      bias[e] = e < p.E ? __ldg(p.bias + e) : 0.f;
+      bias[e] = e < p.E ? route_ld32(p.bias + e) : 0.f;
     }
   }
   __syncthreads();
