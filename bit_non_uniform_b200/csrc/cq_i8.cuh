@@ -214,10 +214,13 @@ struct I8Pass {
 
 // The ring of weight units in shared memory: slot q % slots holds unit q of
 // the CTA's passes, numbered through.  Unit q is copied by producer warp
-// q % kI8Producers and multiplied by streaming warp q % (slots / 2), and slots
-// is a multiple of both: a slot is always filled by one warp and emptied by
-// one warp, in order, so that a wait on its parity never meets the phase
-// before.
+// q % kI8Producers and multiplied by streaming warp q % i8_streamers(slots),
+// and slots is a multiple of both: a slot is always filled by one warp and
+// emptied by one warp, in order, so that a wait on its parity never meets the
+// phase before.
+__device__ __forceinline__ int i8_streamers(int slots) {
+  return slots <= kI8Warps ? slots : slots / 2;
+}
 struct I8Ring {
   uint32_t data, full, empty;      // shared addresses: units, barriers
   int slots;
@@ -299,7 +302,7 @@ __device__ __forceinline__ void i8_consume(const I8Ring& ring, const uint8_t* ri
                                            int stride, int* acc, uint32_t q0, I8Turn& turn) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int W = ring.slots / 2;
+  const int W = i8_streamers(ring.slots);
   if (warp >= W) return;
   const int nk = (K + kI8Unit - 1) / kI8Unit;
   const int total = ps.tiles() * nk;
