@@ -358,6 +358,11 @@ static int i8_moe_stage(I8MoeParams p, const int8_t* w, const float* wscale, int
   p.nt = i8_tokens_per_pass(K, plan);
   if (p.T <= 8 && p.nt > 8) p.nt = 8;
   if (p.R < p.nt) p.nt = p.R;
+  // nanoseconds x 10 per row and per route of a row, at 50 bytes a nanosecond
+  // and 7 us a pass
+  constexpr int rpt = DOWN ? 16 : 8;
+  p.wt_row = static_cast<int>((DOWN ? K : 2 * K) / 50) + 1;
+  p.wt_route = 70000 / (kI8AccBytes / 64 * rpt);
   const int smem = i8_layout(p, p.nt, K, plan);
   return p.nt <= 8 ? launch_i8_moe<DOWN, 1>(p, sms, smem, s)
                    : launch_i8_moe<DOWN, 2>(p, sms, smem, s);

@@ -466,8 +466,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 // ---------------------------------------------------------------------------
 // Both launches read the routes themselves: the experts in use, each with its
 // routes, cut into chunks of at most `nt` routes.  A chunk multiplies every
-// row of its expert, so the work is chunks x rows, split evenly over the
-// CTAs.
+// row of its expert, so the work is chunks x rows, split over the CTAs in
+// equal shares of an estimated cost.
 //   gate/up: xq = codes of the chunk's tokens; g, u per (row, route);
 //            h[route][row] = RN32(silu(g) u) with g, u and silu in FP64, so
 //            that the codes of the second quantization are those of any other
@@ -489,6 +489,7 @@ struct I8MoeParams {
   int T, k, R, E;
   int64_t H, I;
   int nt;                   // routes per chunk
+  int wt_row, wt_route;     // i8_weight
   int out_bf16, clear_y;
   int stride;               // i8_row_stride of the stage's K
   int xs_off, acc_off;      // staged rows and accumulators, behind the ring
@@ -508,20 +509,22 @@ struct I8Plan {
   int16_t* route;       // routes by expert
   int16_t* dense;       // each route's expert, as an index into `expert`, or -1
   int16_t* rank;        // its place among the expert's routes
-  int* n;               // experts in use, chunks
+  int* cost;            // i8_weight of the chunks before each expert, and of all
+  int* n;               // experts in use, chunks, this CTA's first row and the next one's
 };
 
 __host__ __device__ constexpr int i8_plan_routes(int R) { return (R + 31) / 32 * 32; }
 __host__ __device__ constexpr int i8_plan_words(int E) { return (E + 31) / 32; }
 __host__ __device__ constexpr int i8_plan_bytes(int R, int E) {
-  return (i8_plan_words(E) * 6 + i8_plan_routes(R) * 14 + 4 * 2 + 2 * 4 + 15) / 16 * 16;
+  return (i8_plan_words(E) * 6 + i8_plan_routes(R) * 18 + 4 * 2 + 6 * 4 + 15) / 16 * 16;
 }
 
 __device__ __forceinline__ I8Plan i8_plan_at(uint8_t* at, int R, int E) {
   const int r = i8_plan_routes(R), w = i8_plan_words(E);
   I8Plan s;
   s.n = reinterpret_cast<int*>(at);
-  s.bits = reinterpret_cast<uint32_t*>(s.n + 2);
+  s.cost = s.n + 4;
+  s.bits = reinterpret_cast<uint32_t*>(s.cost + r + 2);
   s.pref = reinterpret_cast<int16_t*>(s.bits + w);
   s.expert = s.pref + w;
   s.cnt = s.expert + r;
@@ -533,6 +536,44 @@ __device__ __forceinline__ I8Plan i8_plan_at(uint8_t* at, int R, int E) {
   return s;
 }
 
+// What a row of a chunk costs: its bytes, a tenth more when its routes take
+// two blocks of MMA columns, and its share of the passes (the accumulators
+// hold fewer rows, the more routes a chunk has; a pass ends with a gap of some
+// 7 us).  Split by rows alone, the CTAs of experts with 9 to 13 routes finished
+// at 390 to 410 us, all others at 345 (16 tokens, 64 experts 7168 x 3072).
+__device__ __forceinline__ int i8_weight(const I8MoeParams& p, int cnt) {
+  return p.wt_row * (cnt > 8 ? 11 : 10) + p.wt_route * cnt;
+}
+// ... and the chunks of an expert with `cnt` routes.
+__device__ __forceinline__ int i8_expert_weight(const I8MoeParams& p, int cnt) {
+  if (cnt == 0) return 0;
+  const int whole = (cnt - 1) / p.nt;
+  return whole * i8_weight(p, p.nt) + i8_weight(p, cnt - whole * p.nt);
+}
+
+// The row of the chunks' rows, numbered through, at which CTA b of n begins:
+// equal shares of the cost, or of the rows for the few routes of the short
+// plan.  FP32 is exact enough (a row or two) and quick, and
+// every step rounds monotonously, so that the CTAs' ranges join.
+__device__ __forceinline__ int i8_begin(const I8MoeParams& p, const I8Plan& s, int ne, int nc,
+                                        int rows, int b, int n) {
+  if (b == n || ne == 0) return nc * rows;
+  const float at = __fdiv_rn(__fmul_rn(s.cost[ne], b), n);
+  int d0 = 0, d1 = ne;                     // the expert: largest d that begins at or before it
+  while (d1 - d0 > 1) {
+    const int mid = (d0 + d1) >> 1;
+    if (static_cast<float>(s.cost[mid]) <= at) d0 = mid; else d1 = mid;
+  }
+  float left = __fsub_rn(at, s.cost[d0]);
+  const int cnt = s.off[d0 + 1] - s.off[d0], whole = (cnt - 1) / p.nt;
+  const float w = i8_weight(p, p.nt);
+  int c = static_cast<int>(__fdiv_rn(left, w));
+  c = c < whole ? c : whole;
+  left = __fsub_rn(left, __fmul_rn(c, w));
+  const float share = __fdiv_rn(left, i8_weight(p, c < whole ? p.nt : cnt - whole * p.nt));
+  const int row = static_cast<int>(__fmul_rn(share, rows));
+  return (s.chunk[d0] + c) * rows + min(max(row, 0), rows);
+}
 __device__ __forceinline__ int warp_inclusive_sum(int v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -545,7 +586,7 @@ __device__ __forceinline__ int warp_inclusive_sum(int v) {
 
 // The plan of at most 32 routes, by the first warp (experts in the order of
 // their first route; the order only decides which CTA works on what).
-__device__ __forceinline__ void i8_plan_small(const I8MoeParams& p, const I8Plan& s) {
+__device__ __forceinline__ void i8_plan_small(const I8MoeParams& p, const I8Plan& s, int rows) {
   const int lane = threadIdx.x;
   if (lane < 32) {
     int id = lane < p.R ? p.ids[lane] : -1;
@@ -572,16 +613,17 @@ __device__ __forceinline__ void i8_plan_small(const I8MoeParams& p, const I8Plan
       s.n[1] = ch;
       s.off[ne] = static_cast<int16_t>(off);
       s.chunk[ne] = static_cast<int16_t>(ch);
+      // floor(rows b / n): where CTAs and chunks divide evenly, none gets two
+      // chunks to stage
+      const int total = ch * rows, n = gridDim.x, b = blockIdx.x, q = total / n, r = total - q * n;
+      s.n[2] = b * q + b * r / n;
+      s.n[3] = (b + 1) * q + (b + 1) * r / n;
     }
   }
   __syncthreads();
 }
 
-__device__ __forceinline__ void i8_plan(const I8MoeParams& p, const I8Plan& s) {
-  if (p.R <= 32) {
-    i8_plan_small(p, s);
-    return;
-  }
+__device__ __forceinline__ void i8_plan_large(const I8MoeParams& p, const I8Plan& s, int rows) {
   const int tid = threadIdx.x;
   const int words = (p.E + 31) / 32;
   for (int i = tid; i < words; i += kI8Threads) s.bits[i] = 0u;
@@ -623,25 +665,32 @@ __device__ __forceinline__ void i8_plan(const I8MoeParams& p, const I8Plan& s) {
       s.rank[r0 + tid] = static_cast<int16_t>(base + before);
       __syncwarp();
     }
-    int off = 0, ch = 0;
+    int off = 0, ch = 0, cost = 0;
     for (int d0 = 0; d0 < ne; d0 += 32) {
       const int cnt = d0 + tid < ne ? s.cnt[d0 + tid] : 0;
       const int chunks = (cnt + p.nt - 1) / p.nt;
       const int a = warp_inclusive_sum(cnt), b = warp_inclusive_sum(chunks);
+      const int weight = i8_expert_weight(p, cnt), c = warp_inclusive_sum(weight);
       if (d0 + tid < ne) {
         s.off[d0 + tid] = static_cast<int16_t>(off + a - cnt);
         s.chunk[d0 + tid] = static_cast<int16_t>(ch + b - chunks);
+        s.cost[d0 + tid] = cost + c - weight;
       }
       off += __shfl_sync(0xffffffffu, a, 31);
       ch += __shfl_sync(0xffffffffu, b, 31);
+      cost += __shfl_sync(0xffffffffu, c, 31);
     }
     if (tid == 0) {
+      s.cost[ne] = cost;
       s.off[ne] = static_cast<int16_t>(off);
       s.chunk[ne] = static_cast<int16_t>(ch);
       s.n[0] = ne;
       s.n[1] = ch;
     }
     __syncwarp();
+    if (tid < 2)
+      s.n[2 + tid] = i8_begin(p, s, ne, ch, rows, static_cast<int>(blockIdx.x) + tid,
+                              static_cast<int>(gridDim.x));
     for (int r = tid; r < p.R; r += 32) {
       const int d = s.dense[r];
       if (d >= 0) s.route[s.off[d] + s.rank[r]] = static_cast<int16_t>(r);
@@ -676,11 +725,12 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   }
   // the second launch may start before the first has ended: the ids are the
   // caller's and were complete before the first began
-  i8_plan(p, s);
-  const int nc = s.n[1];
-  const int64_t W = static_cast<int64_t>(nc) * rows;         // below 2^27
-  int lo = static_cast<int>(W * blockIdx.x / gridDim.x);     // next row of the chunks' rows
-  const int hi = static_cast<int>(W * (blockIdx.x + 1) / gridDim.x);
+  if (p.R <= 32)
+    i8_plan_small(p, s, rows);
+  else
+    i8_plan_large(p, s, rows);
+  int lo = s.n[2];                               // next row of the chunks' rows (below 2^27)
+  const int hi = s.n[3];
 
   // the passes of this CTA: rows [a, a + nr) of a chunk, all with its routes
   struct Work {
