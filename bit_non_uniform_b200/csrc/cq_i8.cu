@@ -363,6 +363,8 @@ static int i8_moe_stage(I8MoeParams p, const int8_t* w, const float* wscale, int
   constexpr int rpt = DOWN ? 16 : 8;
   p.wt_row = static_cast<int>((DOWN ? K : 2 * K) / 50) + 1;
   p.wt_route = 70000 / (kI8AccBytes / 64 * rpt);
+  p.wt_gap = 35000.f / static_cast<float>(DOWN ? p.H : p.I);
+  p.gap_rows = static_cast<int>(3500 * 50 / (DOWN ? K : 2 * K));
   const int smem = i8_layout(p, p.nt, K, plan);
   return p.nt <= 8 ? launch_i8_moe<DOWN, 1>(p, sms, smem, s)
                    : launch_i8_moe<DOWN, 2>(p, sms, smem, s);

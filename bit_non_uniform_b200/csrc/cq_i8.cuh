@@ -490,6 +490,8 @@ struct I8MoeParams {
   int64_t H, I;
   int nt;                   // routes per chunk
   int wt_row, wt_route;     // i8_weight
+  float wt_gap;             // what staging another chunk costs, in units of its rows' weight
+  int gap_rows;             // ... in rows
   int out_bf16, clear_y;
   int stride;               // i8_row_stride of the stage's K
   int xs_off, acc_off;      // staged rows and accumulators, behind the ring
@@ -553,20 +555,25 @@ __device__ __forceinline__ int i8_expert_weight(const I8MoeParams& p, int cnt) {
 
 // The row of the chunks' rows, numbered through, at which CTA b of n begins:
 // equal shares of the cost, or of the rows for the few routes of the short
-// plan.  FP32 is exact enough (a row or two) and quick, and
+// plan.  A CTA whose rows span two chunks stages activations twice (3 to 4 us, for
+// which all others wait), so that chunks are laid out with gaps of
+// that cost between them, at most a CTA's share; a CTA that would begin in a
+// gap begins behind it.  FP32 is exact enough (a row or two) and quick, and
 // every step rounds monotonously, so that the CTAs' ranges join.
 __device__ __forceinline__ int i8_begin(const I8MoeParams& p, const I8Plan& s, int ne, int nc,
                                         int rows, int b, int n) {
   if (b == n || ne == 0) return nc * rows;
-  const float at = __fdiv_rn(__fmul_rn(s.cost[ne], b), n);
+  const float all = s.cost[ne], gap = fminf(p.wt_gap, __fdiv_rn(all, n));
+  const float at = __fdiv_rn(__fmul_rn(__fadd_rn(all, __fmul_rn(nc - 1, gap)), b), n);
+  auto begins = [&](int d) { return __fadd_rn(s.cost[d], __fmul_rn(s.chunk[d], gap)); };
   int d0 = 0, d1 = ne;                     // the expert: largest d that begins at or before it
   while (d1 - d0 > 1) {
     const int mid = (d0 + d1) >> 1;
-    if (static_cast<float>(s.cost[mid]) <= at) d0 = mid; else d1 = mid;
+    if (begins(mid) <= at) d0 = mid; else d1 = mid;
   }
-  float left = __fsub_rn(at, s.cost[d0]);
+  float left = __fsub_rn(at, begins(d0));
   const int cnt = s.off[d0 + 1] - s.off[d0], whole = (cnt - 1) / p.nt;
-  const float w = i8_weight(p, p.nt);
+  const float w = __fadd_rn(i8_weight(p, p.nt), gap);
   int c = static_cast<int>(__fdiv_rn(left, w));
   c = c < whole ? c : whole;
   left = __fsub_rn(left, __fmul_rn(c, w));
@@ -613,11 +620,14 @@ __device__ __forceinline__ void i8_plan_small(const I8MoeParams& p, const I8Plan
       s.n[1] = ch;
       s.off[ne] = static_cast<int16_t>(off);
       s.chunk[ne] = static_cast<int16_t>(ch);
-      // floor(rows b / n): where CTAs and chunks divide evenly, none gets two
-      // chunks to stage
-      const int total = ch * rows, n = gridDim.x, b = blockIdx.x, q = total / n, r = total - q * n;
-      s.n[2] = b * q + b * r / n;
-      s.n[3] = (b + 1) * q + (b + 1) * r / n;
+      const int n = gridDim.x, gap = min(p.gap_rows, ch * rows / n);
+      const int pitch = rows + gap, total = ch * pitch - gap, q = total / n, r = total - q * n;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int b = static_cast<int>(blockIdx.x) + i;
+        const int at = ch > 0 ? b * q + b * r / n : 0, c = at / pitch;
+        s.n[2 + i] = c * rows + min(at - c * pitch, rows);
+      }
     }
   }
   __syncthreads();
