@@ -23,7 +23,7 @@
 //   * every CTA quantizes the few activation rows itself (no separate launch).
 // Loading straight into the consumers' registers (two buffers of 4 KB a warp)
 // kept too little in flight once several tokens made a step's arithmetic
-// longer: 4.8 TB/s at 16 tokens of 64 experts against 6.5 now.  Measured: one
+// longer: 4.8 TB/s at 16 tokens of 64 experts against 6.4 now.  Measured: one
 // token of 16 experts 7168 x 3072 in 170 us, 6.2 TB/s or 96% of the copy rate;
 // 6144 x 7168 for one token in 10.5 us, of which 3.7 are the launch and staging
 // that a small matrix takes too.
@@ -556,10 +556,11 @@ __device__ __forceinline__ int i8_expert_weight(const I8MoeParams& p, int cnt) {
 // The row of the chunks' rows, numbered through, at which CTA b of n begins:
 // equal shares of the cost, or of the rows for the few routes of the short
 // plan.  A CTA whose rows span two chunks stages activations twice (3 to 4 us, for
-// which all others wait), so that chunks are laid out with gaps of
-// that cost between them, at most a CTA's share; a CTA that would begin in a
-// gap begins behind it.  FP32 is exact enough (a row or two) and quick, and
-// every step rounds monotonously, so that the CTAs' ranges join.
+// which all others wait), so that chunks are laid out with gaps of that cost
+// between them, at most a CTA's share; a CTA that would begin in a gap begins
+// behind it: 5 tokens of 40 experts 2064 x 1040 28 us instead of 32.5.  FP32 is
+// exact enough (a row or two) and quick, and every step rounds monotonously, so
+// that the CTAs' ranges join.
 __device__ __forceinline__ int i8_begin(const I8MoeParams& p, const I8Plan& s, int ne, int nc,
                                         int rows, int b, int n) {
   if (b == n || ne == 0) return nc * rows;
