@@ -5,6 +5,7 @@
 #include "cq.h"
 #include "cq_host.h"
 #include "cq_i8.cuh"
+#include "cq_i8_group.cuh"
 #include "cq_i8_tc.cuh"
 
 namespace cq {
@@ -169,7 +170,7 @@ static int i8_encode(CUtensorMap* map, const void* base, int rank, const cuuint6
                      const cuuint64_t* strides, const cuuint32_t* box) {
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return CQ_ERR_CUDA;
-  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank),
                   const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -319,16 +320,38 @@ static int i8_gemm_impl(const void* x, const float* absmax, int64_t M, const int
 // ---------------------------------------------------------------------------
 struct I8MoePlan {
   int64_t T;                 // tokens of one launch
-  size_t o_y, total;         // h comes first
+  int nt;                    // routes per tile on the tensor cores; 0: streamed
+  int tiles;                 // ... and tiles, at most
+  size_t o_y, o_xq, o_sx, o_route, o_tile, o_n, total;         // h comes first
 };
 
-static I8MoePlan i8_moe_plan(int64_t T, int k, int64_t H, int64_t I) {
-  I8MoePlan m;
-  const int64_t most = kI8MaxRoutes / k;
+// Streamed up to 16 routes per expert on average (one chunk each), then on
+// the tensor cores.
+static I8MoePlan i8_moe_plan(int64_t T, int k, int E, int64_t H, int64_t I) {
+  I8MoePlan m = {};
+  const int64_t routes = T * k;
+  if (routes > 16 * static_cast<int64_t>(E))
+    m.nt = routes > 192 * static_cast<int64_t>(E) ? 256 : routes > 48 * static_cast<int64_t>(E) ? 128 : 64;
+  const int64_t most = (m.nt ? kGpMaxRoutes : kI8MaxRoutes) / k;
   m.T = T < most ? T : most;
   const size_t R = static_cast<size_t>(m.T) * k;
-  m.o_y = i8_round256(R * I * sizeof(float));
-  m.total = m.o_y + i8_round256(R * H * sizeof(float));
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += i8_round256(bytes);
+    return o;
+  };
+  take(R * I * sizeof(float));
+  m.o_y = take(R * H * sizeof(float));
+  if (m.nt) {
+    m.tiles = static_cast<int>(R / m.nt + (R < static_cast<size_t>(E) ? R : E));
+    m.o_xq = take(R * (H > I ? H : I));
+    m.o_sx = take(R * sizeof(float));
+    m.o_route = take(R * sizeof(int));
+    m.o_tile = take(m.tiles * sizeof(int4));
+    m.o_n = take(2 * sizeof(int));
+  }
+  m.total = at;
   return m;
 }
 
@@ -370,6 +393,86 @@ static int i8_moe_stage(I8MoeParams p, const int8_t* w, const float* wscale, int
                    : launch_i8_moe<DOWN, 2>(p, sms, smem, s);
 }
 
+// The weights [E][rows][K] of a stage: boxes of 128 rows of an expert (down),
+// or of 8 groups of 8 gate rows and the 8 up rows that belong to them.  What
+// is outside an expert's rows reads 0.
+static int encode_i8_experts(CUtensorMap* map, const int8_t* w, bool down, int64_t E, int64_t rows,
+                             int64_t K) {
+  const cuuint64_t k = static_cast<cuuint64_t>(K), n = static_cast<cuuint64_t>(rows),
+                   e = static_cast<cuuint64_t>(E);
+  if (down) {
+    const cuuint64_t dims[3] = {k, n, e};
+    const cuuint64_t strides[2] = {k, n * k};
+    const cuuint32_t box[3] = {kTcBlock, kRows, 1};
+    return i8_encode(map, w, 3, dims, strides, box);
+  }
+  const cuuint64_t dims[5] = {k, 8, 2, n / 8, e};
+  const cuuint64_t strides[4] = {k, n * k, 8 * k, 2 * n * k};
+  const cuuint32_t box[5] = {kTcBlock, 8, 2, kRows / 16, 1};
+  return i8_encode(map, w, 5, dims, strides, box);
+}
+
+template <int NT, bool DOWN>
+static int i8_group_stage(I8GroupParams p, const int8_t* w, const float* wscale, int tiles,
+                          cudaStream_t s) {
+  static std::atomic<uint64_t> smem_set{0};
+  if (!ensure_smem_limit(i8_group_kernel<NT, DOWN>, I8GroupCfg<NT>::SMEM, smem_set))
+    return CQ_ERR_CUDA;
+  const int64_t K = DOWN ? p.I : p.H, rows = DOWN ? p.H : p.I, per = DOWN ? kRows : kRows / 2;
+  CUtensorMap xmap, wmap;
+  int st = encode_i8_rows(&xmap, p.xq, p.R, K, NT);
+  if (st == CQ_OK) st = encode_i8_experts(&wmap, w, DOWN, p.E, rows, K);
+  if (st != CQ_OK) return st;
+  p.wscale = wscale;
+  p.n_rt = static_cast<int>((rows + per - 1) / per);
+  p.nkb = static_cast<int>((K + kTcBlock - 1) / kTcBlock);
+  st = launch_pdl(i8_group_rows_kernel<DOWN>, dim3(static_cast<unsigned>(p.R)),
+                  dim3(kGpRowThreads), 0, s, p);
+  if (st != CQ_OK) return st;
+  return launch_pdl(i8_group_kernel<NT, DOWN>,
+                    dim3(static_cast<unsigned>(tiles) * static_cast<unsigned>(p.n_rt)),
+                    dim3(kTcThreads), I8GroupCfg<NT>::SMEM, s, p, xmap, wmap);
+}
+
+template <int NT>
+static int i8_group_nt(const I8GroupParams& p, const int8_t* w_gu, const float* s_gu,
+                       const int8_t* w_dn, const float* s_dn, int tiles, cudaStream_t s) {
+  const int st = i8_group_stage<NT, false>(p, w_gu, s_gu, tiles, s);
+  return st != CQ_OK ? st : i8_group_stage<NT, true>(p, w_dn, s_dn, tiles, s);
+}
+
+// The routes' outputs of `q`'s tokens on the tensor cores.
+static int i8_group(const I8MoeParams& q, const I8MoePlan& m, uint8_t* ws, const int8_t* w_gu,
+                    const float* s_gu, const int8_t* w_dn, const float* s_dn, cudaStream_t s) {
+  static std::atomic<uint64_t> smem_set{0};
+  if (!ensure_smem_limit(i8_group_plan_kernel, kI8MaxExperts * 4, smem_set)) return CQ_ERR_CUDA;
+  I8GroupParams p = {};
+  p.tokens = q.tokens;
+  p.ids = q.ids;
+  p.h = q.h;
+  p.y = q.y;
+  p.xq = reinterpret_cast<int8_t*>(ws + m.o_xq);
+  p.sx = reinterpret_cast<float*>(ws + m.o_sx);
+  p.route = reinterpret_cast<int*>(ws + m.o_route);
+  p.tile = reinterpret_cast<int4*>(ws + m.o_tile);
+  p.n = reinterpret_cast<int*>(ws + m.o_n);
+  p.k = q.k;
+  p.R = q.R;
+  p.E = q.E;
+  p.H = static_cast<int>(q.H);
+  p.I = static_cast<int>(q.I);
+  p.nt = m.nt;
+  p.clear_y = q.clear_y;
+  p.timeout_ns = kDefaultTimeoutNs;
+  const int st = launch_pdl(i8_group_plan_kernel, dim3(1), dim3(kGpPlanThreads), p.E * 4, s, p);
+  if (st != CQ_OK) return st;
+  switch (m.nt) {
+    case 64: return i8_group_nt<64>(p, w_gu, s_gu, w_dn, s_dn, m.tiles, s);
+    case 128: return i8_group_nt<128>(p, w_gu, s_gu, w_dn, s_dn, m.tiles, s);
+    default: return i8_group_nt<256>(p, w_gu, s_gu, w_dn, s_dn, m.tiles, s);
+  }
+}
+
 }  // namespace cq
 
 using namespace cq;
@@ -399,7 +502,7 @@ extern "C" CQ_API int cq_linear_i8(const uint16_t* x, int64_t M, const int8_t* w
 
 extern "C" CQ_API size_t cq_moe_i8_workspace_size(int64_t T, int k, int E, int64_t H, int64_t I) {
   if (validate_i8_moe(T, k, E, H, I) != CQ_OK) return 0;
-  return i8_moe_plan(T, k, H, I).total;
+  return i8_moe_plan(T, k, E, H, I).total;
 }
 
 extern "C" CQ_API int cq_moe_i8(const uint16_t* tokens, int64_t T, const int32_t* topk_ids,
@@ -421,7 +524,7 @@ extern "C" CQ_API int cq_moe_i8(const uint16_t* tokens, int64_t T, const int32_t
     return CQ_ERR_UNSUPPORTED;
   const int sms = num_sms();
   if (sms <= 0) return CQ_ERR_CUDA;
-  const I8MoePlan m = i8_moe_plan(T, k, H, I);
+  const I8MoePlan m = i8_moe_plan(T, k, E, H, I);
   if (ws_bytes < m.total) return CQ_ERR_WORKSPACE;
   if (!out && !route_out) return CQ_OK;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -443,9 +546,12 @@ extern "C" CQ_API int cq_moe_i8(const uint16_t* tokens, int64_t T, const int32_t
     p.out = out ? static_cast<uint8_t*>(out) + t * H * os : nullptr;
     p.out_bf16 = out_dtype == CQ_DTYPE_BF16;
     p.clear_y = route_out != nullptr;
-    st = i8_moe_stage<false>(p, w_gu, s_gu, sms, s);
-    if (st != CQ_OK) return st;
-    st = i8_moe_stage<true>(p, w_dn, s_dn, sms, s);
+    if (m.nt) {
+      st = i8_group(p, m, ws, w_gu, s_gu, w_dn, s_dn, s);
+    } else {
+      st = i8_moe_stage<false>(p, w_gu, s_gu, sms, s);
+      if (st == CQ_OK) st = i8_moe_stage<true>(p, w_dn, s_dn, sms, s);
+    }
     if (st != CQ_OK) return st;
     if (!out) continue;
     const int64_t n = p.T * (H / 4);

@@ -246,6 +246,7 @@ MOE = [
     (16,  4, 5,  7168, 48,  0.0, False),      # 16 staged tokens leave a short ring
     (14,  3, 4,  64,   8208, 0.3, False),
     (9,   2, 3,  9216, 9232, 0.0, True),
+    (16,  1, 1,  16400, 32, 0.0, False),
 ]
 
 
@@ -270,6 +271,91 @@ def test_moe_matches_fp64(cq, T, k, E, H, I, dropped, bf16):
     only, none = cq.cq_moe_i8(x, ids, None, *lw, combine=False, workspace=ws)
     assert none is None and torch.equal(only, ro)
     assert cq.device_error() == (0, 0)
+
+
+# more than 16 routes per expert: the tensor cores, with tiles of 64, 128 and
+# 256 routes
+MOE_MANY = [
+    (33,   1, 2,  16,   16,  0.0, False),      # one 16-byte block of K each
+    (100,  2, 5,  528,  272, 0.2, True),       # up to 64 routes a tile
+    (101,  3, 3,  400,  144, 0.0, False),      # 101 routes: one tile, not full
+    (257,  2, 2,  272,  80,  0.3, False),      # 257 routes: a tile of one
+    (129,  1, 4,  4112, 48,  0.0, True),       # rows longer than a thread keeps
+    (40,   2, 2,  64,   8208, 0.0, False),
+    (700,  2, 70, 64,   64,  0.5, False),      # many experts, tiles nearly empty
+    (4200, 4, 40, 32,   16,  0.1, False),      # more routes than one launch takes
+]
+
+
+@pytest.mark.parametrize("T,k,E,H,I,dropped,bf16", MOE_MANY)
+def test_moe_many_routes_match_fp64(cq, T, k, E, H, I, dropped, bf16):
+    assert T * k > 16 * E
+    test_moe_matches_fp64(cq, T, k, E, H, I, dropped, bf16)
+
+
+@pytest.mark.parametrize("T", [30, 80, 200])
+def test_moe_many_routes_give_the_bits_of_a_few(cq, T):
+    """A token's outputs do not depend on how many others share the call; all
+    to one expert, dropped routes between, other experts empty."""
+    g = gen(T)
+    k, E, H, I = 2, 3, 640, 208
+    x, lw = tokens(g, T, H), layer(g, E, H, I)
+    ids = torch.full((T, k), 1, dtype=torch.int32, device="cuda")
+    ids[::3, 0] = -1
+    ids[::7] = E
+    w = torch.randn(T, k, generator=g, device="cuda")
+    ro, out = cq.cq_moe_i8(x, ids, w, *lw)
+    for t in range(0, T, 9):
+        few = cq.cq_moe_i8(x[t:t + 9].contiguous(), ids[t:t + 9].contiguous(),
+                           w[t:t + 9].contiguous(), *lw)
+        assert torch.equal(few[0], ro[t * k:(t + 9) * k]) and torch.equal(few[1], out[t:t + 9])
+    assert bool((ro.view(T, k, H)[::7] == 0).all()) and bool((out[::7] == 0).all())
+    ids.fill_(-1)
+    ro, out = cq.cq_moe_i8(x, ids, w, *lw)
+    assert bool((ro == 0).all()) and bool((out == 0).all())
+    assert cq.device_error() == (0, 0)
+
+
+def test_moe_many_routes_hide_no_overflow(cq):
+    g = gen(21)
+    T, k, E, H, I = 60, 2, 4, 512, 64
+    x, lw = tokens(g, T, H), layer(g, E, H, I)
+    ids, w = distinct_ids(g, T, E, k), torch.ones(T, k, device="cuda")
+    clean = cq.cq_moe_i8(x, ids, w, *lw)[0]
+    for bad_row in (torch.full((H,), float("inf"), device="cuda"), x[1].float() * 1e30):
+        bad = x.clone()
+        bad[1] = bad_row.to(torch.bfloat16)
+        ro, out = cq.cq_moe_i8(bad, ids, w, *lw)
+        assert not bool(torch.isfinite(ro[k:2 * k]).any())
+        assert torch.equal(ro[:k], clean[:k]) and torch.equal(ro[2 * k:], clean[2 * k:])
+
+
+def test_moe_many_routes_captured_and_on_another_stream(cq):
+    g = gen(22)
+    T, k, E, H, I = 70, 2, 3, 256, 96
+    lw = layer(g, E, H, I)
+    xs = [tokens(g, T, H) for _ in range(2)]
+    ids = [distinct_ids(g, T, E, k) for _ in range(2)]
+    w = torch.rand(T, k, generator=g, device="cuda")
+    want = [cq.cq_moe_i8(xs[i], ids[i], w, *lw, route_out=False)[1] for i in range(2)]
+    ws = cq.moe_i8_workspace(T, k, E, H, I)
+    x, i = xs[0].clone(), ids[0].clone()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        out = cq.cq_moe_i8(x, i, w, *lw, route_out=False, workspace=ws)[1]
+        twice = cq.cq_moe_i8(x, i, w, *lw, route_out=False, workspace=ws)[1]
+    for n in (0, 1, 0):
+        x.copy_(xs[n])
+        i.copy_(ids[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[n]) and torch.equal(twice, want[n])
+    with torch.cuda.stream(s):
+        other = cq.cq_moe_i8(xs[1], ids[1], w, *lw, route_out=False)[1]
+    s.synchronize()
+    assert torch.equal(other, want[1])
 
 
 def test_moe_all_routes_dropped(cq):
