@@ -511,7 +511,7 @@ def moe_i8_workspace(T, k, E, H, I, device="cuda"):
 
 def cq_moe_i8(tokens, topk_ids, topk_w, w_gu, s_gu, w_dn, s_dn, out_dtype: int = F32,
               route_out=True, combine=True, workspace=None, stream=None):
-    """Routed-expert FFN of one MoE layer on INT8 experts, for a few tokens:
+    """Routed-expert FFN of one MoE layer on INT8 experts:
     w_gu int8 [E][2I][H], s_gu [E][2I], w_dn int8 [E][H][I], s_dn [E][H].
     Returns (route_out, out) as cq_moe_grouped_gemm does."""
     if _direct is not None and combine and stream is None and (route_out is False

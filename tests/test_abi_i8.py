@@ -85,11 +85,20 @@ def test_moe_refuses_bad_arguments(cq):
     assert moe(cq, T=0) == 0
 
 
+@pytest.mark.parametrize("k,E,H,I", [(8, 64, 7168, 2048), (2, 4, 64, 32), (16, 1000, 512, 256),
+                                     (1, 1, 16, 16), (7, 40, 4096, 1536), (1000, 16384, 16, 32)])
+def test_moe_workspace_serves_fewer_tokens(cq, k, E, H, I):
+    """Whichever kernels a number of tokens takes: no fewer tokens need more."""
+    f = cq.lib().cq_moe_i8_workspace_size
+    sizes = [f(T, k, E, H, I) for T in list(range(300)) + list(range(300, 20000, 37)) + [1 << 20]]
+    assert sizes == sorted(sizes) and sizes[1] > 0
+
+
 def test_moe_workspace(cq):
     f = cq.lib().cq_moe_i8_workspace_size
     assert f(2, 2, 4, 64, 32) >= 2 * 2 * (64 + 32) * 4
     # one launch's routes bound the size
-    assert f(100000, 8, 4, 64, 32) == f(128, 8, 4, 64, 32)
+    assert f(100000, 8, 4, 64, 32) == f(2048, 8, 4, 64, 32)
     for bad in ((-1, 2, 4, 64, 32), (2, 0, 4, 64, 32), (2, 2, 0, 64, 32), (2, 2, 4, 72, 32),
                 (2, 2, 4, 64, 40), (2, 1025, 4, 64, 32)):
         assert f(*bad) == 0, bad

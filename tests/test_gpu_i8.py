@@ -247,6 +247,7 @@ MOE = [
     (14,  3, 4,  64,   8208, 0.3, False),
     (9,   2, 3,  9216, 9232, 0.0, True),
     (16,  1, 1,  16400, 32, 0.0, False),
+    (9,   1, 2,  9216, 9232, 0.0, False),
 ]
 
 
