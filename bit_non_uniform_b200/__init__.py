@@ -588,7 +588,7 @@ def cq_moe_route(logits, k: int, bias=None, scoring: int = SCORE_SOFTMAX, renorm
     L = _lib or lib()
     pl = _tensor("logits", logits, dt, (T, E), index)
     pb = None if bias is None else _tensor("bias", bias, torch.float32, (E,), index)
-    shape = (T, max(k, 0))
+    shape = (T, min(max(k, 0), E))               # a larger k is refused below
     ids = logits.new_empty(shape, dtype=torch.int32)
     w = logits.new_empty(shape, dtype=torch.float32)
     _check(L.cq_moe_route(pl, F32 if dt is torch.float32 else BF16, T, E, k, pb, scoring,

@@ -163,7 +163,7 @@ PyObject* route(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const c10::DeviceIndex dev = l->get_device();
   const int64_t T = l->size(0), E = l->size(1);
   const bool f32 = l->scalar_type() == at::kFloat;
-  if (dev != c10::cuda::current_device() || k < 0 || E > INT32_MAX ||
+  if (dev != c10::cuda::current_device() || k < 0 || k > E || E > INT32_MAX ||
       !is(l, f32 ? at::kFloat : at::kBFloat16, {T, E}, dev))
     return none();
   const at::Tensor* b = nullptr;

@@ -769,3 +769,12 @@ def test_compiled_and_general_calls_agree(cq, monkeypatch):
             m.setattr(cq, "_direct", None)
             for a, b in zip(fast, calls(T)):
                 assert a.dtype == b.dtype and a.shape == b.shape and torch.equal(a, b)
+
+
+def test_route_refuses_more_experts_than_there_are_without_allocating(cq):
+    logits = torch.randn(4096, 8, device="cuda")
+    for k in (9, 2 ** 31 - 1):
+        with pytest.raises((ValueError, RuntimeError)) as e:
+            cq.cq_moe_route(logits, k)
+        assert not isinstance(e.value, torch.OutOfMemoryError), k
+    assert cq.cq_moe_route(logits, 8)[0].shape == (4096, 8)
