@@ -327,11 +327,13 @@ struct I8MoePlan {
 
 // Streamed for few routes per expert, on the tensor cores from 5 on average:
 // 64 experts 7168 x 2048 take 387 us streamed and 378 there at 4 routes each,
-// 492 and 421 at 8, 802 and 452 at 16; 16 experts 4096 x 1536 69 and 73 at 4,
+// 492 and 413 at 8, 802 and 439 at 16; 16 experts 4096 x 1536 69 and 73 at 4,
 // 76 and 73 at 6.  Four launches more cost 4 us, so that layers whose weights
 // take no longer than that change at 16: 4 experts 512 x 256 13.3 and 17.3 us
-// at 8 routes each, 17.3 and 17.7 at 16.  Tiles of about the mean, a half more
-// at most.
+// at 8 routes each, 17.3 and 17.7 at 16.  Tiles of 64 routes up to 96
+// each: 531 us against 562 with 128 at 48 routes each, 720 against 722 at 96,
+// 1007 against 831 at 128.  (256 routes, one CTA per SM: 1470 us at 256 each,
+// 1293 with 128.)
 static I8MoePlan i8_moe_plan(int64_t T, int k, int E, int64_t H, int64_t I) {
   I8MoePlan m = {};
   const int64_t e = E;
@@ -339,7 +341,7 @@ static I8MoePlan i8_moe_plan(int64_t T, int k, int E, int64_t H, int64_t I) {
   const int64_t most = (sorted ? kGpMaxRoutes : kI8MaxRoutes) / k;
   m.T = T < most ? T : most;
   const size_t R = static_cast<size_t>(m.T) * k;
-  if (sorted) m.nt = m.T * k > 192 * e ? 256 : m.T * k > 48 * e ? 128 : 64;
+  if (sorted) m.nt = m.T * k > 96 * e ? 128 : 64;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -474,8 +476,7 @@ static int i8_group(const I8MoeParams& q, const I8MoePlan& m, uint8_t* ws, const
   if (st != CQ_OK) return st;
   switch (m.nt) {
     case 64: return i8_group_nt<64>(p, w_gu, s_gu, w_dn, s_dn, m.tiles, s);
-    case 128: return i8_group_nt<128>(p, w_gu, s_gu, w_dn, s_dn, m.tiles, s);
-    default: return i8_group_nt<256>(p, w_gu, s_gu, w_dn, s_dn, m.tiles, s);
+    default: return i8_group_nt<128>(p, w_gu, s_gu, w_dn, s_dn, m.tiles, s);
   }
 }
 

@@ -4,9 +4,9 @@
 // The streamed layer reads an expert's weights from L2 again for every 16
 // routes and multiplies on the legacy tensor path: 1024 tokens of 64 experts
 // 7168 x 2048 (128 routes each) took 6.3 ms, here 0.83.  HBM bounds it up to
-// 32 routes each (256 tokens: 504 us, the weights alone 436), then the copies
-// from L2 into shared memory and tiles that are not full (2048 tokens: 1.47 ms,
-// 30% of the tensor rate).  The steps:
+// 32 routes each (256 tokens: 482 us, the weights alone 436), then the copies
+// from L2 into shared memory and tiles that are not full (2048 tokens: 1.29 ms,
+// 34% of the tensor rate).  The steps:
 //   i8_group_plan_kernel   sorts the routes by expert and lists the tiles (up
 //                          to NT routes of one expert);
 //   i8_group_rows_kernel   quantizes the sorted rows: a token once per route,
@@ -181,18 +181,19 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// Up to 128 routes two CTAs share an SM, so that one's epilogue runs beside
-// the other's products.
+// Two or three CTAs share an SM, so that one's epilogue runs beside the
+// others' products: with tiles of 64 routes 482 us with three, 504 with two
+// (256 tokens, 64 experts 7168 x 2048, top 8).
 template <int NT>
 struct I8GroupCfg {
-  static constexpr int CTAS = NT <= 128 ? 2 : 1;
+  static constexpr int CTAS = NT == 64 ? 3 : 2;
   static constexpr int A_BYTES = kRows * kTcBlock;
   static constexpr int STAGE = A_BYTES + NT * kTcBlock;
   static constexpr int MISC = 1024 + NT * 8;                   // barriers, scales, routes
-  static constexpr int STAGES = ((CTAS == 2 ? 112 : 220) * 1024 - 1024 - MISC) / STAGE;
+  static constexpr int STAGES = ((CTAS == 3 ? 75 : 112) * 1024 - 1024 - MISC) / STAGE;
   static constexpr int SMEM = 1024 + STAGES * STAGE + MISC;
   static_assert(STAGES >= 3 && STAGE % 1024 == 0 && 16 * STAGES + 24 <= 1024, "shared memory");
-  static_assert(NT >= 32 && CTAS * NT <= kTmemCols && (NT & (NT - 1)) == 0, "TMEM columns");
+  static_assert((NT == 64 || NT == 128) && CTAS * NT <= kTmemCols, "TMEM columns");
 };
 
 template <int NT, bool DOWN>

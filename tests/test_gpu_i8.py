@@ -274,13 +274,13 @@ def test_moe_matches_fp64(cq, T, k, E, H, I, dropped, bf16):
     assert cq.device_error() == (0, 0)
 
 
-# more than 16 routes per expert: the tensor cores, with tiles of 64, 128 and
-# 256 routes
+# more than 16 routes per expert: the tensor cores, with tiles of 64 and 128
+# routes
 MOE_MANY = [
     (33,   1, 2,  16,   16,  0.0, False),      # one 16-byte block of K each
     (100,  2, 5,  528,  272, 0.2, True),       # up to 64 routes a tile
     (101,  3, 3,  400,  144, 0.0, False),      # 101 routes: one tile, not full
-    (257,  2, 2,  272,  80,  0.3, False),      # 257 routes: a tile of one
+    (257,  2, 2,  272,  80,  0.3, False),      # several tiles of an expert
     (129,  1, 4,  4112, 48,  0.0, True),       # rows longer than a thread keeps
     (40,   2, 2,  64,   8208, 0.0, False),
     (700,  2, 70, 64,   64,  0.5, False),      # many experts, tiles nearly empty
