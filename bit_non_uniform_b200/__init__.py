@@ -44,6 +44,7 @@ class CQError(RuntimeError):
 
 
 _lib = None
+_direct = None          # the compiled INT8 calls (_cq_torch), loaded with the library
 
 
 class MatrixDesc(ctypes.Structure):
@@ -56,8 +57,10 @@ class ExpertDesc(ctypes.Structure):
 
 
 def lib():
-    """Load libcq.so (raises if it has not been built)."""
-    global _lib
+    """Load libcq.so (raises if it has not been built), and the compiled calls
+    that link against it.  Not before: a process that imports the package in
+    order to build the library must not hold the one it replaces."""
+    global _lib, _direct
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -102,6 +105,10 @@ def lib():
         f = getattr(L, name)
         f.restype = res
         f.argtypes = args
+    try:
+        from . import _cq_torch as _direct
+    except ImportError:                    # not built: the calls go through Python
+        _direct = None
     _lib = L
     return L
 
@@ -367,11 +374,6 @@ def cq_moe_grouped_gemm(tokens, topk_ids, topk_w, layer, E: int, H: int, I: int,
 # the compiled module, in about half the time; all others go through Python:
 # one test per tensor, the current stream's handle without a Stream object, and
 # no context manager where device and stream are the current ones already.
-try:
-    from . import _cq_torch as _direct
-except ImportError:                        # not built (yet)
-    _direct = None
-
 
 def _direct_result(r, where):
     if type(r) is int:
