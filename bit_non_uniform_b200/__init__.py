@@ -98,6 +98,13 @@ def lib():
         "cq_moe_i8_workspace_size": (sz, [i64, i32, i32, i64, i64]),
         "cq_moe_i8": (i32, [P, i64, P, P, i32, i32, P, P, P, P, i64, i64, i32, P, P, P, sz, P]),
         "cq_moe_route": (i32, [P, i32, i64, i32, i32, P, i32, i32, ctypes.c_float, P, P, P]),
+        "cq_test_product_i8_path": (i32, [i64, i64, i64, i32]),
+        "cq_test_product_i8": (i32, [P, P, i64, P, P, i64, i64, i32, i32, P, P, sz, i32, u64, i32,
+                                     P]),
+        "cq_test_moe_i8_path": (i32, [i64, i32, i32, i64, i64, ctypes.POINTER(i64)]),
+        "cq_test_moe_i8_workspace_size": (sz, [i64, i32, i32, i64, i64, i32]),
+        "cq_test_moe_i8": (i32, [P, i64, P, P, i32, i32, P, P, P, P, i64, i64, i32, P, P, P, sz,
+                                 i32, u64, i32, P]),
         "cq_test_gemm_path": (i32, [P, i64, P, P, P, i64, i64, i32, i32, i32, i32, i32, P, P,
                                     sz, i32, P]),
     }

@@ -61,7 +61,7 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [
-        os.path.join(INCLUDE, h) for h in ("cq.h", "cq_hooks.h")]
+        os.path.join(INCLUDE, h) for h in ("cq.h", "cq_hooks.h", "cq_hooks_i8.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include "cq.h"
+#include "cq_hooks_i8.h"
 #include "cq_host.h"
 #include "cq_i8.cuh"
 #include "cq_i8_group.cuh"
@@ -16,6 +17,13 @@ static_assert(kI8SmemLimit - 2048 - kI8AccBytes - kI8MinSlots * kI8UnitBytes -
                       i8_plan_bytes(kI8MaxRoutes, kI8MaxExperts) >=
                   i8_row_stride(kI8MaxK),
               "one row");
+
+// What the test hooks choose; a call's own values.
+struct I8Hook {
+  int path = CQ_I8_AUTO;
+  uint64_t timeout_ns = kDefaultTimeoutNs;
+  int withhold = 0;
+};
 
 // The shared memory of a streaming kernel beside its static arrays: a ring of
 // units, `tokens` staged rows, the accumulators, and (MoE) the plan.
@@ -33,14 +41,16 @@ static int i8_tokens_per_pass(int64_t K, int plan) {
 }
 
 template <typename Params>
-static int i8_layout(Params& p, int tokens, int64_t K, int plan) {
+static int i8_layout(Params& p, int tokens, int64_t K, int plan, uint64_t timeout_ns,
+                     bool withhold) {
   p.stride = i8_row_stride(K);
   const int rest = kI8Smem - plan - kI8AccBytes - tokens * p.stride;
   const int slots = rest / kI8UnitBytes < kI8MaxSlots ? rest / kI8UnitBytes : kI8MaxSlots;
   p.slots = slots / kI8MinSlots * kI8MinSlots;   // a multiple of the producers, and even
   p.xs_off = p.slots * kI8UnitBytes;
   p.acc_off = p.xs_off + tokens * p.stride;
-  p.timeout_ns = kDefaultTimeoutNs;
+  p.timeout_ns = timeout_ns;
+  p.withhold = withhold;
   return p.acc_off + kI8AccBytes + plan;
 }
 
@@ -55,11 +65,11 @@ static int validate_i8(int64_t M, int64_t N, int64_t K, int epilogue, int out_dt
 }
 
 template <int SRC>
-static int i8_linear(I8LinearParams p, int sms, cudaStream_t s) {
+static int i8_linear(I8LinearParams p, const I8Hook& hook, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> smem_set{0};
   if (!ensure_smem_limit(i8_linear_kernel<SRC>, kI8Smem, smem_set)) return CQ_ERR_CUDA;
   const int rows = p.swiglu ? p.N / 2 : p.N;
-  const int smem = i8_layout(p, p.M, p.K, 0);
+  const int smem = i8_layout(p, p.M, p.K, 0, hook.timeout_ns, hook.withhold);
   return launch_pdl(i8_linear_kernel<SRC>, dim3(rows < sms ? rows : sms), dim3(kI8Threads), smem,
                     s, p);
 }
@@ -124,7 +134,8 @@ static int64_t i8_block_cost(int nt, int rows_loaded) {
   return mma > copies ? mma : copies;
 }
 
-static I8TcPlan i8_tc_plan(int64_t M, int64_t N, int64_t K, int epilogue, int sms) {
+// `path`: CQ_I8_AUTO, or the kernel to choose the tile of.
+static I8TcPlan i8_tc_plan(int64_t M, int64_t N, int64_t K, int epilogue, int sms, int path) {
   const bool sw = epilogue == CQ_EPI_SWIGLU;
   const int64_t out = sw ? N / 2 : N;
   const int64_t nkb = (K + kTcBlock - 1) / kTcBlock, hbm = N * K / 3400;
@@ -132,7 +143,7 @@ static I8TcPlan i8_tc_plan(int64_t M, int64_t N, int64_t K, int epilogue, int sm
   int64_t cost = INT64_MAX;
   auto consider = [&](bool pair, int nt, int split, int64_t n_rt, int64_t n_tt, int64_t main,
                       int cut, int64_t c) {
-    if (c >= cost) return;
+    if (c >= cost || (path != CQ_I8_AUTO && pair != (path == CQ_I8_PAIR))) return;
     cost = c;
     best = {pair, nt, split, static_cast<int>(n_rt), static_cast<int>(n_tt),
             static_cast<int>(nkb), static_cast<int>(main), cut};
@@ -227,7 +238,8 @@ static int launch_i8_pair(const I8TcParams& p, const CUtensorMap& xmap, const CU
 }
 
 static int i8_tc(const I8LinearParams& q, const I8TcPlan& g, const int8_t* xq,
-                 const float* absmax, bool early_w, int sms, cudaStream_t s) {
+                 const float* absmax, bool early_w, const I8Hook& hook, int sms,
+                 cudaStream_t s) {
   CUtensorMap xmap, xtail, wmap;
   int st = encode_i8_rows(&xmap, xq, q.M, q.K, g.pair ? g.NT / 2 : g.NT);
   if (st != CQ_OK) return st;
@@ -258,7 +270,8 @@ static int i8_tc(const I8LinearParams& q, const I8TcPlan& g, const int8_t* xq,
   p.cut = g.cut;
   p.tail_nt = g.NT / g.cut;
   p.early_w = early_w;
-  p.timeout_ns = kDefaultTimeoutNs;
+  p.withhold = hook.withhold != 0;
+  p.timeout_ns = hook.timeout_ns;
   if (g.pair) return launch_i8_pair(p, xmap, xtail, wmap, sms, s);
   switch (g.NT) {
     case 32: return launch_i8_split<32>(p, xmap, wmap, s);
@@ -269,7 +282,8 @@ static int i8_tc(const I8LinearParams& q, const I8TcPlan& g, const int8_t* xq,
 
 static int i8_gemm_impl(const void* x, const float* absmax, int64_t M, const int8_t* wq,
                         const float* wscale, int64_t N, int64_t K, int epilogue, int out_dtype,
-                        void* y, void* workspace, size_t ws_bytes, bool codes, cudaStream_t s) {
+                        void* y, void* workspace, size_t ws_bytes, bool codes, cudaStream_t s,
+                        const I8Hook& hook = {}) {
   const int st = validate_i8(M, N, K, epilogue, out_dtype);
   if (st != CQ_OK) return st;
   if (M == 0 || N == 0) return CQ_OK;
@@ -290,9 +304,12 @@ static int i8_gemm_impl(const void* x, const float* absmax, int64_t M, const int
   p.K = static_cast<int>(K);
   p.swiglu = epilogue == CQ_EPI_SWIGLU;
   p.out_bf16 = out_dtype == CQ_DTYPE_BF16;
-  if (i8_streams(M, K))
-    return codes ? i8_linear<I8_SRC_CODES>(p, sms, s) : i8_linear<I8_SRC_BF16>(p, sms, s);
-  const I8TcPlan g = i8_tc_plan(M, N, K, epilogue, sms);
+  const bool streams = i8_streams(M, K);
+  if (hook.path == CQ_I8_STREAM && !streams) return CQ_ERR_UNSUPPORTED;
+  if (streams && (hook.path == CQ_I8_AUTO || hook.path == CQ_I8_STREAM))
+    return codes ? i8_linear<I8_SRC_CODES>(p, hook, sms, s)
+                 : i8_linear<I8_SRC_BF16>(p, hook, sms, s);
+  const I8TcPlan g = i8_tc_plan(M, N, K, epilogue, sms, hook.path);
   if (static_cast<int64_t>(g.n_rt) * g.n_tt * g.split >= (int64_t)1 << 28)
     return CQ_ERR_UNSUPPORTED;
   const int8_t* xq = static_cast<const int8_t*>(x);
@@ -312,7 +329,7 @@ static int i8_gemm_impl(const void* x, const float* absmax, int64_t M, const int
   }
   // behind the quantization the weights may be fetched early: it ends only
   // after the kernel before it
-  return i8_tc(p, g, xq, absmax, !codes, sms, s);
+  return i8_tc(p, g, xq, absmax, !codes, hook, sms, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -334,10 +351,13 @@ struct I8MoePlan {
 // each: 531 us against 562 with 128 at 48 routes each, 720 against 722 at 96,
 // 1007 against 831 at 128.  (256 routes, one CTA per SM: 1470 us at 256 each,
 // 1293 with 128.)
-static I8MoePlan i8_moe_plan(int64_t T, int k, int E, int64_t H, int64_t I) {
+static I8MoePlan i8_moe_plan(int64_t T, int k, int E, int64_t H, int64_t I,
+                             int path = CQ_I8_AUTO) {
   I8MoePlan m = {};
   const int64_t e = E;
-  const bool sorted = T * k > e * (3 * H * I > (16 << 20) / E ? 5 : 16);
+  const bool sorted = path == CQ_I8_AUTO
+                          ? T * k > e * (3 * H * I > (16 << 20) / E ? 5 : 16)
+                          : path == CQ_I8_SORTED;
   const int64_t most = (sorted ? kGpMaxRoutes : kI8MaxRoutes) / k;
   m.T = T < most ? T : most;
   const size_t R = static_cast<size_t>(m.T) * k;
@@ -378,9 +398,20 @@ static int launch_i8_moe(const I8MoeParams& p, int grid, int smem, cudaStream_t 
   return launch_pdl(i8_moe_kernel<DOWN, NB>, dim3(grid), dim3(kI8Threads), smem, s, p);
 }
 
+// A launch's share of the hook: the one that loses operands has the whole limit.
 template <bool DOWN>
-static int i8_moe_stage(I8MoeParams p, const int8_t* w, const float* wscale, int sms,
-                        cudaStream_t s) {
+static bool i8_stage_withheld(const I8Hook& hook) {
+  return hook.withhold == (DOWN ? 2 : 1);
+}
+template <bool DOWN>
+static uint64_t i8_stage_limit(const I8Hook& hook) {
+  return hook.withhold == 0 || i8_stage_withheld<DOWN>(hook) ? hook.timeout_ns
+                                                             : hook.timeout_ns / 4;
+}
+
+template <bool DOWN>
+static int i8_moe_stage(I8MoeParams p, const int8_t* w, const float* wscale, const I8Hook& hook,
+                        int sms, cudaStream_t s) {
   const int64_t K = DOWN ? p.I : p.H;
   p.w = w;
   p.wscale = wscale;
@@ -396,7 +427,8 @@ static int i8_moe_stage(I8MoeParams p, const int8_t* w, const float* wscale, int
   p.wt_route = 70000 / (kI8AccBytes / 64 * rpt);
   p.wt_gap = 35000.f / static_cast<float>(DOWN ? p.H : p.I);
   p.gap_rows = static_cast<int>(3500 * 50 / (DOWN ? K : 2 * K));
-  const int smem = i8_layout(p, p.nt, K, plan);
+  const int smem = i8_layout(p, p.nt, K, plan, i8_stage_limit<DOWN>(hook),
+                             i8_stage_withheld<DOWN>(hook));
   return p.nt <= 8 ? launch_i8_moe<DOWN, 1>(p, sms, smem, s)
                    : launch_i8_moe<DOWN, 2>(p, sms, smem, s);
 }
@@ -421,8 +453,8 @@ static int encode_i8_experts(CUtensorMap* map, const int8_t* w, bool down, int64
 }
 
 template <int NT, bool DOWN>
-static int i8_group_stage(I8GroupParams p, const int8_t* w, const float* wscale, int tiles,
-                          cudaStream_t s) {
+static int i8_group_stage(I8GroupParams p, const int8_t* w, const float* wscale,
+                          const I8Hook& hook, int tiles, cudaStream_t s) {
   static std::atomic<uint64_t> smem_set{0};
   if (!ensure_smem_limit(i8_group_kernel<NT, DOWN>, I8GroupCfg<NT>::SMEM, smem_set))
     return CQ_ERR_CUDA;
@@ -432,6 +464,8 @@ static int i8_group_stage(I8GroupParams p, const int8_t* w, const float* wscale,
   if (st == CQ_OK) st = encode_i8_experts(&wmap, w, DOWN, p.E, rows, K);
   if (st != CQ_OK) return st;
   p.wscale = wscale;
+  p.withhold = i8_stage_withheld<DOWN>(hook);
+  p.timeout_ns = i8_stage_limit<DOWN>(hook);
   p.n_rt = static_cast<int>((rows + per - 1) / per);
   p.nkb = static_cast<int>((K + kTcBlock - 1) / kTcBlock);
   st = launch_pdl(i8_group_rows_kernel<DOWN>, dim3(static_cast<unsigned>(p.R)),
@@ -444,14 +478,16 @@ static int i8_group_stage(I8GroupParams p, const int8_t* w, const float* wscale,
 
 template <int NT>
 static int i8_group_nt(const I8GroupParams& p, const int8_t* w_gu, const float* s_gu,
-                       const int8_t* w_dn, const float* s_dn, int tiles, cudaStream_t s) {
-  const int st = i8_group_stage<NT, false>(p, w_gu, s_gu, tiles, s);
-  return st != CQ_OK ? st : i8_group_stage<NT, true>(p, w_dn, s_dn, tiles, s);
+                       const int8_t* w_dn, const float* s_dn, const I8Hook& hook, int tiles,
+                       cudaStream_t s) {
+  const int st = i8_group_stage<NT, false>(p, w_gu, s_gu, hook, tiles, s);
+  return st != CQ_OK ? st : i8_group_stage<NT, true>(p, w_dn, s_dn, hook, tiles, s);
 }
 
 // The routes' outputs of `q`'s tokens on the tensor cores.
 static int i8_group(const I8MoeParams& q, const I8MoePlan& m, uint8_t* ws, const int8_t* w_gu,
-                    const float* s_gu, const int8_t* w_dn, const float* s_dn, cudaStream_t s) {
+                    const float* s_gu, const int8_t* w_dn, const float* s_dn,
+                    const I8Hook& hook, cudaStream_t s) {
   static std::atomic<uint64_t> smem_set{0};
   if (!ensure_smem_limit(i8_group_plan_kernel, kI8MaxExperts * 4, smem_set)) return CQ_ERR_CUDA;
   I8GroupParams p = {};
@@ -471,13 +507,69 @@ static int i8_group(const I8MoeParams& q, const I8MoePlan& m, uint8_t* ws, const
   p.I = static_cast<int>(q.I);
   p.nt = m.nt;
   p.clear_y = q.clear_y;
-  p.timeout_ns = kDefaultTimeoutNs;
   const int st = launch_pdl(i8_group_plan_kernel, dim3(1), dim3(kGpPlanThreads), p.E * 4, s, p);
   if (st != CQ_OK) return st;
   switch (m.nt) {
-    case 64: return i8_group_nt<64>(p, w_gu, s_gu, w_dn, s_dn, m.tiles, s);
-    default: return i8_group_nt<128>(p, w_gu, s_gu, w_dn, s_dn, m.tiles, s);
+    case 64: return i8_group_nt<64>(p, w_gu, s_gu, w_dn, s_dn, hook, m.tiles, s);
+    default: return i8_group_nt<128>(p, w_gu, s_gu, w_dn, s_dn, hook, m.tiles, s);
   }
+}
+
+static int i8_moe_impl(const uint16_t* tokens, int64_t T, const int32_t* topk_ids,
+                       const float* topk_w, int k, int E, const int8_t* w_gu, const float* s_gu,
+                       const int8_t* w_dn, const float* s_dn, int64_t H, int64_t I, int out_dtype,
+                       float* route_out, void* out, void* workspace, size_t ws_bytes,
+                       cudaStream_t s, const I8Hook& hook = {}) {
+  int st = validate_i8_moe(T, k, E, H, I);
+  if (st != CQ_OK) return st;
+  if (out_dtype != CQ_DTYPE_F32 && out_dtype != CQ_DTYPE_BF16) return CQ_ERR_INVALID_ARG;
+  if (T == 0) return CQ_OK;
+  if (!tokens || !topk_ids || !w_gu || !s_gu || !w_dn || !s_dn || !workspace)
+    return CQ_ERR_INVALID_ARG;
+  if (out && !topk_w) return CQ_ERR_INVALID_ARG;
+  if (!aligned(tokens, 16) || !aligned(topk_ids, 4) || !aligned(w_gu, 16) || !aligned(s_gu, 4) ||
+      !aligned(w_dn, 16) || !aligned(s_dn, 4) || !aligned(workspace, 256) ||
+      (topk_w && !aligned(topk_w, 4)) || (route_out && !aligned(route_out, 16)) ||
+      (out && !aligned(out, 16)))
+    return CQ_ERR_UNSUPPORTED;
+  const int sms = num_sms();
+  if (sms <= 0) return CQ_ERR_CUDA;
+  const I8MoePlan m = i8_moe_plan(T, k, E, H, I, hook.path);
+  if (ws_bytes < m.total) return CQ_ERR_WORKSPACE;
+  if (!out && !route_out) return CQ_OK;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int os = out_dtype == CQ_DTYPE_BF16 ? 2 : 4;
+  for (int64_t t = 0; t < T; t += m.T) {
+    I8MoeParams p = {};
+    p.T = static_cast<int>(T - t < m.T ? T - t : m.T);
+    p.k = k;
+    p.R = p.T * k;
+    p.E = E;
+    p.H = H;
+    p.I = I;
+    p.tokens = tokens + t * H;
+    p.ids = topk_ids + t * k;
+    p.topk_w = topk_w ? topk_w + t * k : nullptr;
+    p.h = reinterpret_cast<float*>(ws);
+    p.y = route_out ? route_out + t * k * H : reinterpret_cast<float*>(ws + m.o_y);
+    p.out = out ? static_cast<uint8_t*>(out) + t * H * os : nullptr;
+    p.out_bf16 = out_dtype == CQ_DTYPE_BF16;
+    p.clear_y = route_out != nullptr;
+    if (m.nt) {
+      st = i8_group(p, m, ws, w_gu, s_gu, w_dn, s_dn, hook, s);
+    } else {
+      st = i8_moe_stage<false>(p, w_gu, s_gu, hook, sms, s);
+      if (st == CQ_OK) st = i8_moe_stage<true>(p, w_dn, s_dn, hook, sms, s);
+    }
+    if (st != CQ_OK) return st;
+    if (!out) continue;
+    const int64_t n = p.T * (H / 4);
+    st = launch_pdl(i8_combine_kernel,
+                    dim3(static_cast<unsigned>((n + kI8CombineThreads - 1) / kI8CombineThreads)),
+                    dim3(kI8CombineThreads), 0, s, p);
+    if (st != CQ_OK) return st;
+  }
+  return CQ_OK;
 }
 
 }  // namespace cq
@@ -517,55 +609,66 @@ extern "C" CQ_API int cq_moe_i8(const uint16_t* tokens, int64_t T, const int32_t
                                 const float* s_gu, const int8_t* w_dn, const float* s_dn,
                                 int64_t H, int64_t I, int out_dtype, float* route_out, void* out,
                                 void* workspace, size_t ws_bytes, void* stream) {
-  int st = validate_i8_moe(T, k, E, H, I);
-  if (st != CQ_OK) return st;
-  if (out_dtype != CQ_DTYPE_F32 && out_dtype != CQ_DTYPE_BF16) return CQ_ERR_INVALID_ARG;
-  if (T == 0) return CQ_OK;
-  if (!tokens || !topk_ids || !w_gu || !s_gu || !w_dn || !s_dn || !workspace)
-    return CQ_ERR_INVALID_ARG;
-  if (out && !topk_w) return CQ_ERR_INVALID_ARG;
-  if (!aligned(tokens, 16) || !aligned(topk_ids, 4) || !aligned(w_gu, 16) || !aligned(s_gu, 4) ||
-      !aligned(w_dn, 16) || !aligned(s_dn, 4) || !aligned(workspace, 256) ||
-      (topk_w && !aligned(topk_w, 4)) || (route_out && !aligned(route_out, 16)) ||
-      (out && !aligned(out, 16)))
-    return CQ_ERR_UNSUPPORTED;
-  const int sms = num_sms();
-  if (sms <= 0) return CQ_ERR_CUDA;
+  return i8_moe_impl(tokens, T, topk_ids, topk_w, k, E, w_gu, s_gu, w_dn, s_dn, H, I, out_dtype,
+                     route_out, out, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------------------
+// test hooks (declared in cq_hooks_i8.h)
+// ---------------------------------------------------------------------------
+static I8Hook i8_hook(int path, uint64_t timeout_ns, int withhold) {
+  I8Hook hook;
+  hook.path = path;
+  if (timeout_ns) hook.timeout_ns = timeout_ns;
+  hook.withhold = withhold;
+  return hook;
+}
+
+extern "C" CQ_API int cq_test_product_i8_path(int64_t M, int64_t N, int64_t K, int epilogue) {
+  if (validate_i8(M, N, K, epilogue, CQ_DTYPE_F32) != CQ_OK || M == 0 || N == 0) return 0;
+  if (i8_streams(M, K)) return CQ_I8_STREAM;
+  int sms = num_sms();
+  if (sms <= 0) sms = 148;
+  return i8_tc_plan(M, N, K, epilogue, sms, CQ_I8_AUTO).pair ? CQ_I8_PAIR : CQ_I8_SPLIT;
+}
+
+extern "C" CQ_API int cq_test_product_i8(const void* x, const float* absmax, int64_t M,
+                                         const int8_t* wq, const float* wscale, int64_t N,
+                                         int64_t K, int epilogue, int out_dtype, void* y,
+                                         void* workspace, size_t ws_bytes, int path,
+                                         uint64_t timeout_ns, int withhold, void* stream) {
+  if (path < CQ_I8_AUTO || path > CQ_I8_PAIR) return CQ_ERR_INVALID_ARG;
+  return i8_gemm_impl(x, absmax, M, wq, wscale, N, K, epilogue, out_dtype, y, workspace, ws_bytes,
+                      absmax != nullptr, static_cast<cudaStream_t>(stream),
+                      i8_hook(path, timeout_ns, withhold));
+}
+
+static bool i8_moe_path_ok(int path) {
+  return path == CQ_I8_AUTO || path == CQ_I8_STREAM || path == CQ_I8_SORTED;
+}
+
+extern "C" CQ_API int cq_test_moe_i8_path(int64_t T, int k, int E, int64_t H, int64_t I,
+                                          int64_t* tokens_per_launch) {
+  if (validate_i8_moe(T, k, E, H, I) != CQ_OK || T == 0) return 0;
   const I8MoePlan m = i8_moe_plan(T, k, E, H, I);
-  if (ws_bytes < m.total) return CQ_ERR_WORKSPACE;
-  if (!out && !route_out) return CQ_OK;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int os = out_dtype == CQ_DTYPE_BF16 ? 2 : 4;
-  for (int64_t t = 0; t < T; t += m.T) {
-    I8MoeParams p = {};
-    p.T = static_cast<int>(T - t < m.T ? T - t : m.T);
-    p.k = k;
-    p.R = p.T * k;
-    p.E = E;
-    p.H = H;
-    p.I = I;
-    p.tokens = tokens + t * H;
-    p.ids = topk_ids + t * k;
-    p.topk_w = topk_w ? topk_w + t * k : nullptr;
-    p.h = reinterpret_cast<float*>(ws);
-    p.y = route_out ? route_out + t * k * H : reinterpret_cast<float*>(ws + m.o_y);
-    p.out = out ? static_cast<uint8_t*>(out) + t * H * os : nullptr;
-    p.out_bf16 = out_dtype == CQ_DTYPE_BF16;
-    p.clear_y = route_out != nullptr;
-    if (m.nt) {
-      st = i8_group(p, m, ws, w_gu, s_gu, w_dn, s_dn, s);
-    } else {
-      st = i8_moe_stage<false>(p, w_gu, s_gu, sms, s);
-      if (st == CQ_OK) st = i8_moe_stage<true>(p, w_dn, s_dn, sms, s);
-    }
-    if (st != CQ_OK) return st;
-    if (!out) continue;
-    const int64_t n = p.T * (H / 4);
-    st = launch_pdl(i8_combine_kernel,
-                    dim3(static_cast<unsigned>((n + kI8CombineThreads - 1) / kI8CombineThreads)),
-                    dim3(kI8CombineThreads), 0, s, p);
-    if (st != CQ_OK) return st;
-  }
-  return CQ_OK;
+  if (tokens_per_launch) *tokens_per_launch = m.T;
+  return m.nt ? CQ_I8_SORTED : CQ_I8_STREAM;
+}
+
+extern "C" CQ_API size_t cq_test_moe_i8_workspace_size(int64_t T, int k, int E, int64_t H,
+                                                       int64_t I, int path) {
+  if (validate_i8_moe(T, k, E, H, I) != CQ_OK || !i8_moe_path_ok(path)) return 0;
+  return i8_moe_plan(T, k, E, H, I, path).total;
+}
+
+extern "C" CQ_API int cq_test_moe_i8(const uint16_t* tokens, int64_t T, const int32_t* topk_ids,
+                                     const float* topk_w, int k, int E, const int8_t* w_gu,
+                                     const float* s_gu, const int8_t* w_dn, const float* s_dn,
+                                     int64_t H, int64_t I, int out_dtype, float* route_out,
+                                     void* out, void* workspace, size_t ws_bytes, int path,
+                                     uint64_t timeout_ns, int withhold, void* stream) {
+  if (!i8_moe_path_ok(path)) return CQ_ERR_INVALID_ARG;
+  return i8_moe_impl(tokens, T, topk_ids, topk_w, k, E, w_gu, s_gu, w_dn, s_dn, H, I, out_dtype,
+                     route_out, out, workspace, ws_bytes, static_cast<cudaStream_t>(stream),
+                     i8_hook(path, timeout_ns, withhold));
 }

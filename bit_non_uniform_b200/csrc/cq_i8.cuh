@@ -59,6 +59,16 @@ __host__ __device__ constexpr int i8_row_stride(int64_t K) {
   return static_cast<int>((K + kI8Unit - 1) / kI8Unit * kI8Unit) + 64;
 }
 
+// A bounded wait of a whole warp: every lane waits, then the lanes vote, so
+// that they leave together and with one answer (alone, each leaves the spin in
+// its own time, and one may see the phase complete where another gives up).
+// Warp-wide instructions and barriers follow these waits.
+__device__ __forceinline__ bool i8_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
+                                             uint64_t timeout_ns, int site) {
+  const bool ok = *abort == 0 && wait_phase(bar, parity, abort, timeout_ns, site);
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
 // Barrier of the consumers.
 __device__ __forceinline__ void i8_sync() {
   asm volatile("bar.sync 1, 512;" ::: "memory");
@@ -229,9 +239,10 @@ struct I8Ring {
 };
 
 // Set up by one thread, before a barrier of the whole CTA.
-__device__ __forceinline__ void i8_ring_init(const I8Ring& r) {
+// `withhold` (a test hook): the first slot waits for an arrival that never comes.
+__device__ __forceinline__ void i8_ring_init(const I8Ring& r, int withhold) {
   for (int i = 0; i < r.slots; ++i) {
-    mbar_init(r.full + 8 * i, 32);          // the lanes of its producer
+    mbar_init(r.full + 8 * i, 32 + (i == 0 ? withhold : 0));     // the lanes of its producer
     mbar_init(r.empty + 8 * i, 1);
   }
   *r.abort_flag = 0;
@@ -263,8 +274,8 @@ __device__ __forceinline__ void i8_produce(const I8Ring& ring, const I8Pass& ps,
   int u = static_cast<int>(turn.q - q0);
   int tile = u / nk, kk = u - tile * nk;
   for (; u < total; u += kI8Producers) {
-    if (!wait_phase(ring.empty + 8 * turn.slot, (turn.round & 1u) ^ 1u, ring.abort_flag,
-                    ring.timeout_ns, SITE_I8_SLOT_EMPTY))
+    if (!i8_wait_warp(ring.empty + 8 * turn.slot, (turn.round & 1u) ^ 1u, ring.abort_flag,
+                      ring.timeout_ns, SITE_I8_SLOT_EMPTY))
       return;
     const int k = kk * kI8Unit + lane * 16;
     if (k < K) {
@@ -317,8 +328,8 @@ __device__ __forceinline__ void i8_consume(const I8Ring& ring, const uint8_t* ri
   int u = static_cast<int>(turn.q - q0);
   int tile = u / nk, kk = u - tile * nk;
   for (; u < total; u += W) {
-    if (*ring.abort_flag || !wait_phase(ring.full + 8 * turn.slot, turn.round & 1u,
-                                        ring.abort_flag, ring.timeout_ns, SITE_I8_SLOT_FULL))
+    if (!i8_wait_warp(ring.full + 8 * turn.slot, turn.round & 1u, ring.abort_flag,
+                      ring.timeout_ns, SITE_I8_SLOT_FULL))
       return;
     const uint8_t* const w = ring_data + turn.slot * kI8UnitBytes + g * kI8Pitch + t * 16;
     const int8_t* const y0 = x0 + kk * kI8Unit;
@@ -382,6 +393,7 @@ struct I8LinearParams {
   int stride;               // i8_row_stride(K)
   int xs_off, acc_off;      // staged rows and accumulators, behind the ring
   int slots;
+  int withhold;             // i8_ring_init
   uint64_t timeout_ns;
 };
 
@@ -410,7 +422,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   };
   const I8Ring ring = {smem_u32(i8_smem), smem_u32(s_bar), smem_u32(s_bar + kI8MaxSlots), p.slots,
                        p.timeout_ns, &s_abort};
-  if (tid == 0) i8_ring_init(ring);
+  if (tid == 0) i8_ring_init(ring, p.withhold);
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
@@ -496,6 +508,7 @@ struct I8MoeParams {
   int stride;               // i8_row_stride of the stage's K
   int xs_off, acc_off;      // staged rows and accumulators, behind the ring
   int slots;
+  int withhold;             // i8_ring_init
   uint64_t timeout_ns;
 };
 
@@ -729,7 +742,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const int nk = (K + kI8Unit - 1) / kI8Unit;
   const I8Ring ring = {smem_u32(i8_smem), smem_u32(s_bar), smem_u32(s_bar + kI8MaxSlots), p.slots,
                        p.timeout_ns, &s_abort};
-  if (tid == 0) i8_ring_init(ring);
+  if (tid == 0) i8_ring_init(ring, p.withhold);
   if constexpr (!DOWN) {
     griddep_wait();
     griddep_launch_dependents();

@@ -47,6 +47,7 @@ struct I8GroupParams {
   int nt;
   int n_rt, nkb;            // row tiles, blocks of K
   int clear_y;
+  int withhold;             // test hook: the first stage waits for an arrival that never comes
   uint64_t timeout_ns;
 };
 
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(kTcThreads, I8GroupCfg<NT>::CTAS)
 
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_full + 8 * s, s == 0 ? 1 + p.withhold : 1);
       mbar_init(bar_empty + 8 * s, 1);
     }
     mbar_init(bar_dfull, 1);
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kTcThreads, I8GroupCfg<NT>::CTAS)
       s_sx[c] = c < tile.z ? p.sx[tile.y + c] : 0.f;
       if constexpr (DOWN) s_route[c] = c < tile.z ? p.route[tile.y + c] : 0;
     }
-    bool ok = wait_phase(bar_dfull, 0, abort_flag, tmo, SITE_I8_DFULL);
+    bool ok = i8_wait_warp(bar_dfull, 0, abort_flag, tmo, SITE_I8_DFULL);
     ok = tc_epilogue_vote(ok) && *abort_flag == 0;             // also orders s_sx, s_route
     tc_fence_after();
     const uint32_t daddr = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);

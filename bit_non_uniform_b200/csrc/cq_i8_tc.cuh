@@ -177,10 +177,11 @@ struct I8TcParams {
   // each of the others is cut into `cut` parts of tail_nt tokens
   int nt, main_tiles, cut, tail_nt;
   int early_w;              // the weights may be read before griddep_wait
+  int withhold;             // test hook: the first stage waits for an arrival that never comes
   uint64_t timeout_ns;
 };
 
-// AND-vote and barrier of the epilogue's threads.
+// AND-vote and barrier of the epilogue's threads (whole warps).
 __device__ __forceinline__ bool tc_epilogue_vote(bool ok) {
   uint32_t r;
   asm volatile(
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_full + 8 * s, s == 0 ? 1 + p.withhold : 1);
       mbar_init(bar_empty + 8 * s, 1);
     }
     mbar_init(bar_dfull, 1);
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     griddep_wait();
     l = i8_lane(p, rt0, tt * NT, NT);
     i8_load_scales(p, l.m0, l.mv, NT, s_sx);
-    ok = wait_phase(bar_dfull, 0, abort_flag, tmo, SITE_I8_DFULL);
+    ok = i8_wait_warp(bar_dfull, 0, abort_flag, tmo, SITE_I8_DFULL);
     ok = tc_epilogue_vote(ok) && *abort_flag == 0;         // also orders s_sx
     tc_fence_after();
     const uint32_t daddr = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -565,7 +566,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_full + 8 * s, s == 0 ? 1 + p.withhold : 1);
       mbar_init(bar_empty + 8 * s, 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -698,8 +699,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const I8Lane l = i8_lane(p, (tile.rt * 2 + rank) * cta_rows, tile.m0, tile.nt);
       i8_load_scales(p, l.m0, l.mv, tile.nt, s_sx);
       const uint32_t db = done & 1u;
-      const bool ok = wait_phase(bar_dfull + 8 * db, (done >> 1) & 1u, abort_flag, tmo,
-                                 SITE_I8_DFULL);
+      const bool ok = i8_wait_warp(bar_dfull + 8 * db, (done >> 1) & 1u, abort_flag, tmo,
+                                   SITE_I8_DFULL);
       if (!tc_epilogue_vote(ok)) break;                     // also orders s_sx
       tc_fence_after();
       const uint32_t daddr = tmem_base + lane_addr + db * C::NT;
