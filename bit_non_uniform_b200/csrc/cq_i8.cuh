@@ -49,7 +49,10 @@ constexpr int kI8MaxRoutes = 1024;           // routes of one launch of the MoE 
 constexpr int kI8MaxExperts = 16384;
 constexpr int kI8SmemLimit = 227 * 1024;
 
+// Waits of the streaming kernels; the MoE layer's second launch adds
+// kI8SecondSite.
 enum I8Site : int { SITE_I8_SLOT_EMPTY = 54, SITE_I8_SLOT_FULL = 55 };
+constexpr int kI8SecondSite = 2;
 
 // Bytes between two activation rows in shared memory: whole units (zeros past
 // K, where a unit's weights are whatever the slot held before), plus 64 so
@@ -234,6 +237,7 @@ __device__ __forceinline__ int i8_streamers(int slots) {
 struct I8Ring {
   uint32_t data, full, empty;      // shared addresses: units, barriers
   int slots;
+  int site;                        // 0 or kI8SecondSite
   uint64_t timeout_ns;
   volatile int* abort_flag;
 };
@@ -274,8 +278,12 @@ __device__ __forceinline__ void i8_produce(const I8Ring& ring, const I8Pass& ps,
   int u = static_cast<int>(turn.q - q0);
   int tile = u / nk, kk = u - tile * nk;
   for (; u < total; u += kI8Producers) {
+    // the first round fills free slots; waiting for one to be emptied has its
+    // limit, which must not run while a preceding kernel does (a no-op where
+    // the CTA has waited for it already)
+    if (turn.round == 1u) griddep_wait();
     if (!i8_wait_warp(ring.empty + 8 * turn.slot, (turn.round & 1u) ^ 1u, ring.abort_flag,
-                      ring.timeout_ns, SITE_I8_SLOT_EMPTY))
+                      ring.timeout_ns, SITE_I8_SLOT_EMPTY + ring.site))
       return;
     const int k = kk * kI8Unit + lane * 16;
     if (k < K) {
@@ -329,7 +337,7 @@ __device__ __forceinline__ void i8_consume(const I8Ring& ring, const uint8_t* ri
   int tile = u / nk, kk = u - tile * nk;
   for (; u < total; u += W) {
     if (!i8_wait_warp(ring.full + 8 * turn.slot, turn.round & 1u, ring.abort_flag,
-                      ring.timeout_ns, SITE_I8_SLOT_FULL))
+                      ring.timeout_ns, SITE_I8_SLOT_FULL + ring.site))
       return;
     const uint8_t* const w = ring_data + turn.slot * kI8UnitBytes + g * kI8Pitch + t * 16;
     const int8_t* const y0 = x0 + kk * kI8Unit;
@@ -421,7 +429,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     return ps;
   };
   const I8Ring ring = {smem_u32(i8_smem), smem_u32(s_bar), smem_u32(s_bar + kI8MaxSlots), p.slots,
-                       p.timeout_ns, &s_abort};
+                       0, p.timeout_ns, &s_abort};
   if (tid == 0) i8_ring_init(ring, p.withhold);
   __syncthreads();
   griddep_wait();
@@ -741,7 +749,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   constexpr int rpt = DOWN ? 16 : 8;
   const int nk = (K + kI8Unit - 1) / kI8Unit;
   const I8Ring ring = {smem_u32(i8_smem), smem_u32(s_bar), smem_u32(s_bar + kI8MaxSlots), p.slots,
-                       p.timeout_ns, &s_abort};
+                       DOWN ? kI8SecondSite : 0, p.timeout_ns, &s_abort};
   if (tid == 0) i8_ring_init(ring, p.withhold);
   if constexpr (!DOWN) {
     griddep_wait();

@@ -14,6 +14,7 @@ ERR_TIMEOUT = 4
 STREAM, SPLIT, PAIR, SORTED = 1, 2, 3, 4
 LIMIT = 20_000_000                   # 20 ms
 STREAM_SITES = (54, 55)              # a slot of the ring that stays full, or empty
+SECOND = 2                           # added by the layer's second launch
 TC_SITES = (50, 51, 52, 53)
 
 
@@ -116,9 +117,28 @@ def test_withheld_operands_of_a_layer_time_out(cq, path, T, k, E, H, I, stage):
     assert call(LIMIT, stage) == 0
     status, site = cq.device_error()
     assert status == ERR_TIMEOUT
-    assert site in (STREAM_SITES if path == STREAM else TC_SITES)
+    if path == STREAM:
+        assert site in [s + SECOND * (stage - 1) for s in STREAM_SITES]
+    else:
+        assert site in TC_SITES
     assert cq.device_error() == (0, 0)
     out.zero_()
+    assert call(0, 0) == 0
+    assert cq.device_error() == (0, 0)
+    assert torch.equal(out, want)
+
+
+def test_the_second_launch_does_not_count_the_first_ones_time(cq):
+    """One expert of 16 gate/up pairs keeps 16 CTAs busy, so that the down
+    launch starts on the other SMs at once, fills its ring (28 units a CTA, more
+    than fit) and waits.  The gate/up launch is held for 40 ms; the down
+    launch's limit of 10 ms must not begin before that one has ended."""
+    T, k, E, H, I = 1, 1, 1, 65536, 16
+    call, out, want = layer_call(cq, T, k, E, H, I, STREAM)
+    assert cq.device_error() == (0, 0)
+    assert call(40_000_000, 1) == 0
+    status, site = cq.device_error()
+    assert status == ERR_TIMEOUT and site in STREAM_SITES
     assert call(0, 0) == 0
     assert cq.device_error() == (0, 0)
     assert torch.equal(out, want)
