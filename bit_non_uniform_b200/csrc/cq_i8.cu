@@ -342,22 +342,36 @@ struct I8MoePlan {
   size_t o_y, o_xq, o_sx, o_route, o_tile, o_n, total;         // h comes first
 };
 
-// Streamed for few routes per expert, on the tensor cores from 5 on average:
-// 64 experts 7168 x 2048 take 387 us streamed and 378 there at 4 routes each,
-// 492 and 413 at 8, 802 and 439 at 16; 16 experts 4096 x 1536 69 and 73 at 4,
-// 76 and 73 at 6.  Four launches more cost 4 us, so that layers whose weights
-// take no longer than that change at 16: 4 experts 512 x 256 13.3 and 17.3 us
-// at 8 routes each, 17.3 and 17.7 at 16.  Tiles of 64 routes up to 96
-// each: 531 us against 562 with 128 at 48 routes each, 720 against 722 at 96,
-// 1007 against 831 at 128.  (256 routes, one CTA per SM: 1470 us at 256 each,
-// 1293 with 128.)
+// Streamed or sorted?  Streaming takes one launch less per stage and reads the
+// routes' experts at the HBM's rate, but a CTA stages activations for every
+// chunk it works on, and a launch holds kI8MaxRoutes routes: a second one
+// would read most experts again.  Sorted tiles cost some 5 us more at a few
+// routes and next to nothing per expert.  Measured on weights not in L2,
+// streamed / sorted in us (uniform routes):
+//   * up to 32 routes, which one warp plans: 13.7 / 17.5 (4 experts 512 x 256,
+//     32 routes), 19.6 / 25.4 (16 of 1024 x 1024), 112 / 130 (16 of 7168 x
+//     2048); just above, 20.4 / 17.6 (16 of 512 x 256, 48 routes);
+//   * experts of 2 MB and more, up to 4 routes each: 54 / 55 (128 routes of 32
+//     experts 2048 x 1024), 231 / 238 (of 32 experts 7168 x 2048), 1665 / 1656
+//     (1024 of 256); at 8 each 255 / 242 (256 of 32).  Smaller experts leave no
+//     such range: 45 / 42 at 128 routes of 128 experts 1024 x 512;
+//   * in several streamed launches: 2472 / 1720 at 144 tokens, top 8 of 256
+//     experts 7168 x 2048; 15976 / 5793 at 256 tokens, top 16 of 896.
+// Dropped routes count: the host does not know them.
+// Tiles of 64 routes up to 96 each: 531 us against 562 with 128 at 48 routes
+// each (64 experts 7168 x 2048), 720 against 722 at 96, 1007 against 831 at
+// 128.  (256 routes, one CTA per SM: 1470 us at 256 each, 1293 with 128.)
+static bool i8_moe_sorted(int64_t routes, int64_t E, int64_t H, int64_t I, int k) {
+  if (routes <= 32) return false;
+  return routes > kI8MaxRoutes / k * k || 3 * H * I < (2 << 20) || routes > 4 * E;
+}
+
 static I8MoePlan i8_moe_plan(int64_t T, int k, int E, int64_t H, int64_t I,
                              int path = CQ_I8_AUTO) {
   I8MoePlan m = {};
   const int64_t e = E;
-  const bool sorted = path == CQ_I8_AUTO
-                          ? T * k > e * (3 * H * I > (16 << 20) / E ? 5 : 16)
-                          : path == CQ_I8_SORTED;
+  const bool sorted =
+      path == CQ_I8_AUTO ? i8_moe_sorted(T * k, E, H, I, k) : path == CQ_I8_SORTED;
   const int64_t most = (sorted ? kGpMaxRoutes : kI8MaxRoutes) / k;
   m.T = T < most ? T : most;
   const size_t R = static_cast<size_t>(m.T) * k;

@@ -345,10 +345,12 @@ CQ_API int cq_linear_i8(const uint16_t *x, int64_t M, const int8_t *wq, const fl
 
 /*
  * cq_moe_i8 -- the routed-expert FFN of one MoE layer with INT8 experts.  For
- * a few routes per expert (a decode step) two kernels stream each expert in
- * use once (again for every further 8 to 16 routes of one expert); for more,
- * the routes are sorted by expert and multiplied on the tensor cores; another
- * kernel sums each token's routes.  Both give the same bits.  For every route r = t*k + j with e = topk_ids[t][j]:
+ * a few routes (a decode step) two kernels stream each expert in use once
+ * (again for every further 8 to 16 routes of one expert); for more, the routes
+ * are sorted by expert and multiplied on the tensor cores; another kernel sums
+ * each token's routes.  Both give the same bits.  Dropped routes count when the
+ * kernels are chosen.
+ * For every route r = t*k + j with e = topk_ids[t][j]:
  *   xq, absmax = cq_quant_rows(tokens[t]);
  *   g|u   = RN(absmax / 127) * s_gu[e][n] * (xq . w_gu[e][n])
  *   h     = RN32(silu(g) * u), evaluated in FP64 so that the codes of
@@ -369,9 +371,8 @@ CQ_API int cq_linear_i8(const uint16_t *x, int64_t M, const int8_t *wq, const fl
  * An activation that makes h overflow or NaN makes its route's y_r not finite.
  * A shared expert of the same width is one more expert: id E-1 and weight 1
  * in an extra column of topk_ids.  H and I multiples of 16, at most 131072;
- * k at most 1024; E at most 16384.  More than 1024 streamed routes, or 16384
- * sorted ones, run as successive groups of tokens, each reading its experts
- * again.  Calls that share one
+ * k at most 1024; E at most 16384.  More than 16384 routes run as successive
+ * groups of tokens, each reading its experts again.  Calls that share one
  * workspace must not overlap on the GPU.
  */
 CQ_API size_t cq_moe_i8_workspace_size(int64_t T, int k, int E, int64_t H, int64_t I);

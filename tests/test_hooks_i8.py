@@ -70,3 +70,34 @@ def test_paths(lib):
                  for p in (AUTO, STREAM, SORTED)]
         auto = lib.cq_moe_i8_workspace_size(T, 8, 64, 7168, 2048)
         assert sizes[0] == auto == sizes[1 if T == 16 else 2] and sizes[1] < sizes[2]
+
+
+def moe_path(lib, T, k, E, H, I):
+    n = ctypes.c_int64(0)
+    return lib.cq_test_moe_i8_path(T, k, E, H, I, n), n.value
+
+
+def test_no_layer_is_streamed_in_several_launches(lib):
+    """A streamed launch holds 1024 routes, and a second one would read most
+    experts again: 256 tokens of 896 experts, top 16, would read them 2.8 times."""
+    for k, E, H, I in ((16, 896, 7168, 2048), (8, 256, 7168, 2048), (8, 2048, 2048, 1024),
+                       (8, 16384, 512, 512), (7, 1000, 4096, 1536), (1000, 4000, 2048, 1024)):
+        for T in (1, 2, 3, 60, 64, 72, 128, 129, 146, 147, 160, 256, 300, 512, 4096):
+            path, per = moe_path(lib, T, k, E, H, I)
+            assert path == SORTED or per == T, (T, k, E)
+    assert moe_path(lib, 64, 16, 896, 7168, 2048) == (STREAM, 64)
+    assert moe_path(lib, 65, 16, 896, 7168, 2048) == (SORTED, 65)
+    assert moe_path(lib, 128, 8, 256, 7168, 2048)[0] == STREAM
+    assert moe_path(lib, 129, 8, 256, 7168, 2048)[0] == SORTED
+
+
+def test_small_experts_are_streamed_for_few_routes_only(lib):
+    """Whatever their number: staging activations for every chunk of routes costs
+    more than its rows' weights."""
+    for E, H, I in ((4, 512, 256), (16, 512, 256), (128, 256, 128), (512, 512, 256),
+                    (1024, 64, 80)):
+        assert moe_path(lib, 16, 2, E, H, I)[0] == STREAM, E
+        assert moe_path(lib, 17, 2, E, H, I)[0] == SORTED, E
+    # large ones while their weights bound both
+    assert moe_path(lib, 32, 4, 32, 2048, 1024)[0] == STREAM
+    assert moe_path(lib, 33, 4, 32, 2048, 1024)[0] == SORTED
