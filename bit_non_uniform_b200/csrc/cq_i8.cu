@@ -366,13 +366,23 @@ static bool i8_moe_sorted(int64_t routes, int64_t E, int64_t H, int64_t I, int k
   return routes > kI8MaxRoutes / k * k || 3 * H * I < (2 << 20) || routes > 4 * E;
 }
 
+// Routes of one sorted launch: every further launch reads the experts again,
+// so 128 for each of them (then the products take as long as the weights), at
+// most as many as keep the workspace near 3 GB for rows of 7168.  With 16384
+// for any number of experts 2048 tokens, top 16 of 896 experts 7168 x 2048,
+// took 13.1 ms instead of 7.0.
+static int64_t i8_group_routes(int64_t E) {
+  const int64_t r = 128 * E;
+  return r < 16384 ? 16384 : (r < 65536 ? r : 65536);
+}
+
 static I8MoePlan i8_moe_plan(int64_t T, int k, int E, int64_t H, int64_t I,
                              int path = CQ_I8_AUTO) {
   I8MoePlan m = {};
   const int64_t e = E;
   const bool sorted =
       path == CQ_I8_AUTO ? i8_moe_sorted(T * k, E, H, I, k) : path == CQ_I8_SORTED;
-  const int64_t most = (sorted ? kGpMaxRoutes : kI8MaxRoutes) / k;
+  const int64_t most = (sorted ? i8_group_routes(e) : kI8MaxRoutes) / k;
   m.T = T < most ? T : most;
   const size_t R = static_cast<size_t>(m.T) * k;
   if (sorted) m.nt = m.T * k > 96 * e ? 128 : 64;

@@ -30,7 +30,6 @@ namespace cq {
 constexpr int kGpPlanThreads = 1024;
 constexpr int kGpRowThreads = 256;
 constexpr int kGpRowKeep = 4;              // groups of 8 values kept per thread
-constexpr int kGpMaxRoutes = 16384;        // routes of one launch
 
 struct I8GroupParams {
   const uint16_t* tokens;   // bf16 [T][H]

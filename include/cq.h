@@ -371,9 +371,9 @@ CQ_API int cq_linear_i8(const uint16_t *x, int64_t M, const int8_t *wq, const fl
  * An activation that makes h overflow or NaN makes its route's y_r not finite.
  * A shared expert of the same width is one more expert: id E-1 and weight 1
  * in an extra column of topk_ids.  H and I multiples of 16, at most 131072;
- * k at most 1024; E at most 16384.  More than 16384 routes run as successive
- * groups of tokens, each reading its experts again.  Calls that share one
- * workspace must not overlap on the GPU.
+ * k at most 1024; E at most 16384.  More than 16384 routes, or 128 per expert
+ * up to 65536, run as successive groups of tokens, each reading its experts
+ * again.  Calls that share one workspace must not overlap on the GPU.
  */
 CQ_API size_t cq_moe_i8_workspace_size(int64_t T, int k, int E, int64_t H, int64_t I);
 CQ_API int cq_moe_i8(const uint16_t *tokens, int64_t T, const int32_t *topk_ids,

@@ -101,3 +101,13 @@ def test_small_experts_are_streamed_for_few_routes_only(lib):
     # large ones while their weights bound both
     assert moe_path(lib, 32, 4, 32, 2048, 1024)[0] == STREAM
     assert moe_path(lib, 33, 4, 32, 2048, 1024)[0] == SORTED
+
+
+def test_a_sorted_launch_holds_more_routes_of_more_experts(lib):
+    """Every further launch reads the experts again: 2048 tokens of 896 experts,
+    top 16, are 37 routes each and took two."""
+    assert moe_path(lib, 2048, 16, 896, 7168, 2048) == (SORTED, 2048)
+    assert moe_path(lib, 100000, 16, 896, 7168, 2048) == (SORTED, 4096)
+    assert moe_path(lib, 100000, 8, 256, 7168, 2048) == (SORTED, 4096)
+    assert moe_path(lib, 100000, 8, 64, 7168, 2048) == (SORTED, 2048)
+    assert lib.cq_moe_i8_workspace_size(1 << 20, 16, 896, 7168, 2048) < 3 << 30
