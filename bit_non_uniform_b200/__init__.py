@@ -391,6 +391,8 @@ def _direct_result(r, where):
 def _on_device(index: int, stream):
     """The call's device and stream as the current ones (libcq launches on the
     current device)."""
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
     stack = contextlib.ExitStack()
     stack.enter_context(torch.cuda.device(index))
     if stream is not None:
