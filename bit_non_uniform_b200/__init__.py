@@ -112,8 +112,11 @@ def lib():
         f = getattr(L, name)
         f.restype = res
         f.argtypes = args
+    from .build import built_for
     try:
         from . import _cq_torch as _direct
+        if getattr(_direct, "built_for", None) != built_for():
+            _direct = None
     except ImportError:                    # not built: the calls go through Python
         _direct = None
     _lib = L

@@ -32,12 +32,27 @@ TORCH_LIB = os.path.join(HERE, "_cq_torch.so")
 CXX = os.environ.get("CXX", "g++")
 
 
+def built_for() -> str:
+    """The torch and Python whose C++ and C interfaces the extension uses.  The
+    extension carries this line, and one that carries another is not loaded."""
+    import torch
+    return f"torch {torch.__version__}, python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
+def _torch_stale() -> bool:
+    if not os.path.exists(TORCH_LIB):
+        return True
+    t = os.path.getmtime(TORCH_LIB)
+    if any(os.path.getmtime(d) > t for d in (TORCH_SRC, os.path.join(INCLUDE, "cq.h"))):
+        return True
+    with open(TORCH_LIB, "rb") as f:
+        return built_for().encode() not in f.read()
+
+
 def build_torch(force: bool = False) -> str:
     """The extension links against libcq.so beside it."""
-    if not force and os.path.exists(TORCH_LIB):
-        t = os.path.getmtime(TORCH_LIB)
-        if all(os.path.getmtime(d) <= t for d in (TORCH_SRC, os.path.join(INCLUDE, "cq.h"))):
-            return TORCH_LIB
+    if not force and not _torch_stale():
+        return TORCH_LIB
     import sysconfig
 
     import torch
@@ -47,6 +62,7 @@ def build_torch(force: bool = False) -> str:
     subprocess.check_call([
         CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        f'-DCQ_BUILT_FOR="{built_for()}"',
         "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"),
         "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
         "-I", os.path.join(cuda, "include"), TORCH_SRC, "-o", tmp,

@@ -202,4 +202,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_cq_torch", "libcq calls on torch 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__cq_torch() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__cq_torch() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", CQ_BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

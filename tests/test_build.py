@@ -36,3 +36,45 @@ cq.lib()
 print(mapped(), cq._direct is not None)
 """)
     assert out.splitlines() == ["[] None", "['_cq_torch.so', 'libcq.so'] True"]
+
+
+@pytest.fixture
+def compiles(monkeypatch, tmp_path):
+    """build.py with the extension's place in a new folder; what it would run."""
+    from bit_non_uniform_b200 import build
+    monkeypatch.setattr(build, "TORCH_LIB", str(tmp_path / "_cq_torch.so"))
+    calls = []
+
+    def check_call(cmd):
+        calls.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("new")
+
+    monkeypatch.setattr(build.subprocess, "check_call", check_call)
+    return build, calls
+
+
+def test_an_extension_of_another_torch_is_built_again(compiles):
+    build, calls = compiles
+    for text, runs in ((f"x {build.built_for()} y", 0), ("torch 1.0, python 3.12", 1)):
+        with open(build.TORCH_LIB, "w") as f:
+            f.write(text)
+        build.build_torch()
+        assert len(calls) == runs
+    assert f'-DCQ_BUILT_FOR="{build.built_for()}"' in calls[0]
+    with open(build.TORCH_LIB) as f:
+        assert f.read() == "new"
+
+
+def test_an_extension_of_another_torch_is_not_loaded():
+    code = """
+import sys, types
+if {fake}:
+    sys.modules["bit_non_uniform_b200._cq_torch"] = types.SimpleNamespace(**{fake})
+import bit_non_uniform_b200 as cq
+cq.lib()
+print(cq._direct is None)
+"""
+    for fake in (dict(built_for="torch 1.0"), dict(older=1)):
+        assert python(code.format(fake=fake)).strip() == "True"
+    assert python(code.format(fake={})).strip() == "False"
