@@ -49,8 +49,11 @@ def _torch_stale() -> bool:
         return built_for().encode() not in f.read()
 
 
-def build_torch(force: bool = False) -> str:
-    """The extension links against libcq.so beside it."""
+def build_torch(force: bool = False) -> str | None:
+    """The extension links against libcq.so beside it.  libcq and the binding
+    are complete without it (its calls then go through Python), so that a
+    compiler that fails here is reported and fails nothing else; the extension
+    of older sources is taken away."""
     if not force and not _torch_stale():
         return TORCH_LIB
     import sysconfig
@@ -59,15 +62,23 @@ def build_torch(force: bool = False) -> str:
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(NVCC))
     tmp = TORCH_LIB + f".tmp{os.getpid()}"
-    subprocess.check_call([
-        CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-        f'-DCQ_BUILT_FOR="{built_for()}"',
-        "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"),
-        "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
-        "-I", os.path.join(cuda, "include"), TORCH_SRC, "-o", tmp,
-        "-L", HERE, "-l:libcq.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(root, "lib"),
-        "-ltorch_python", "-ltorch", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+    try:
+        subprocess.check_call([
+            CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DCQ_BUILT_FOR="{built_for()}"',
+            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+            "-I", os.path.join(root, "include"),
+            "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            "-I", os.path.join(cuda, "include"), TORCH_SRC, "-o", tmp,
+            "-L", HERE, "-l:libcq.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(root, "lib"),
+            "-ltorch_python", "-ltorch", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+    except (OSError, subprocess.CalledProcessError) as e:
+        print(f"{os.path.basename(TORCH_LIB)} was not built: {e}", file=sys.stderr)
+        for path in (tmp, TORCH_LIB):
+            if os.path.exists(path):
+                os.remove(path)
+        return None
     os.replace(tmp, TORCH_LIB)
     return TORCH_LIB
 

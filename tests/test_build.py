@@ -78,3 +78,19 @@ print(cq._direct is None)
     for fake in (dict(built_for="torch 1.0"), dict(older=1)):
         assert python(code.format(fake=fake)).strip() == "True"
     assert python(code.format(fake={})).strip() == "False"
+
+
+@pytest.mark.parametrize("error", [FileNotFoundError("no compiler"),
+                                   subprocess.CalledProcessError(1, "g++")])
+def test_the_library_is_built_without_the_extension(compiles, monkeypatch, capfd, error):
+    build, calls = compiles
+    with open(build.TORCH_LIB, "w") as f:
+        f.write("older")
+
+    def check_call(cmd):
+        raise error
+
+    monkeypatch.setattr(build.subprocess, "check_call", check_call)
+    assert build.build() == build.LIB and os.path.exists(build.LIB)
+    assert not os.path.exists(build.TORCH_LIB)
+    assert "_cq_torch.so was not built" in capfd.readouterr().err
