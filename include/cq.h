@@ -368,7 +368,9 @@ CQ_API int cq_linear_i8(const uint16_t *x, int64_t M, const int8_t *wq, const fl
  *   out       [T][H] in out_dtype (may be NULL)
  *   workspace device scratch of cq_moe_i8_workspace_size(...) bytes, 256-byte
  *             aligned
- * An activation that makes h overflow or NaN makes its route's y_r not finite.
+ * An activation that makes h overflow or NaN makes its route's y_r not finite,
+ * and so does an infinite one; a NaN activation has code 0 and does not raise
+ * absmax, as in cq_quant_rows, so that the outputs do not show it.
  * A shared expert of the same width is one more expert: id E-1 and weight 1
  * in an extra column of topk_ids.  H and I multiples of 16, at most 131072;
  * k at most 1024; E at most 16384.  More than 16384 routes, or 128 per expert

@@ -131,3 +131,21 @@ def test_products_on_a_chosen_path(cq, path, M, N, K, swiglu):  # noqa: F811
 ])
 def test_which_kernel_a_product_takes(cq, M, N, K, epi, path):  # noqa: F811
     assert cq.lib().cq_test_product_i8_path(M, N, K, epi) == path
+
+
+@pytest.mark.parametrize("path", [STREAM, SORTED])
+def test_nan_activations_have_code_0(cq, path):  # noqa: F811
+    """A NaN activation does not raise its row's maximum and contributes nothing;
+    a row of NaN is a row of zeros."""
+    T, k, E, H, I = 12, 2, 4, 512, 96
+    g = gen(8)
+    x, lw = tokens(g, T, H), layer(g, E, H, I)
+    ids, w = distinct_ids(g, T, E, k), torch.ones(T, k, device="cuda")
+    x[1, 5] = 0.0
+    x[2] = 0.0
+    clean = moe_on(cq, path, x, ids, w, lw)
+    x[1, 5] = float("nan")
+    x[2] = float("nan")
+    ro, out = moe_on(cq, path, x, ids, w, lw)
+    assert torch.equal(ro, clean[0]) and torch.equal(out, clean[1])
+    assert bool((out[2] == 0).all())
