@@ -59,8 +59,9 @@ def libcq_i8_compute(w_gu: torch.Tensor, s_gu: torch.Tensor, w_dn: torch.Tensor,
                      s_dn: torch.Tensor) -> Compute:
     """The rank's expert computation on the GPU for a layer kept in INT8:
     cq_moe_i8 over its experts (w_gu int8 [E_local][2I][H], s_gu [E_local][2I],
-    w_dn int8 [E_local][H][I], s_dn [E_local][H]), combined per row.  Meant for
-    the few rows of a decode step."""
+    w_dn int8 [E_local][H][I], s_dn [E_local][H]), combined per row.  The ids of
+    other ranks (-1) count when cq_moe_i8 chooses its kernels: the host does not
+    know them."""
     from . import F32, cq_moe_i8
 
     def run(tokens: torch.Tensor, ids: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
