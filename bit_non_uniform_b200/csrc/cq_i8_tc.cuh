@@ -17,9 +17,9 @@
 //     tile (cta_group::2): each CTA loads its 128 weight rows and half of the
 //     tokens, which halves the activation traffic and the shared-memory reads
 //     per MMA.  Two accumulators, so that a tile's epilogue overlaps the next
-//     tile's MMAs.  4096 tokens of 6144 x 7168 take 124 to 128 us (2.8 POP/s at
-//     1.67 GHz), the tensor pipe busy in 85% of the active cycles; the rest
-//     waits for operands, of which an SM takes in about 50 bytes a cycle.
+//     tile's MMAs.  4096 tokens of 6144 x 7168 take 124 to 134 us (2.7 to 2.9
+//     POP/s at 1.65 GHz), the tensor pipe busy in 83% of the active cycles; the
+//     rest waits for operands, of which an SM takes in about 50 bytes a cycle.
 //
 // With SwiGLU a CTA's rows are 8 gate rows, the 8 up rows that belong to
 // them, the next 8 gate rows, and so on, so that gate and up of one output

@@ -105,7 +105,7 @@ PRODUCTS = [
     (300,   1003, 2048, False, False),
     (1025,  514,  784,  True,  True),
     (2049,  1281, 96,   False, False),
-    (16,  300,  8208, False, False),       # long rows staged for 16, 11 and 2 tokens
+    (16,  300,  8208, False, False),       # long rows
     (11,  40,   14000, True, False),
     (2,   100,  99984, False, False),
 ]
@@ -238,12 +238,12 @@ MOE = [
     (3,   4, 6,  2064, 48,  0.0, True),
     (5,   6, 40, 272,  1040, 0.4, False),
     (8,   8, 16, 1024, 144, 0.0, False),
-    (16,  4, 5,  528,  272, 0.2, True),       # up to 16 routes per expert
-    (40,  2, 2,  160,  96,  0.0, False),      # 40 routes per expert: several chunks
-    (300, 5, 7,  48,   32,  0.1, False),      # more routes than one group holds
+    (16,  4, 5,  528,  272, 0.2, True),
+    (40,  2, 2,  160,  96,  0.0, False),
+    (300, 5, 7,  48,   32,  0.1, False),
     (2,   3, 3,  16,   4096, 0.0, False),
-    (20,  1, 1,  16400, 32, 0.0, False),      # long rows: fewer tokens per pass
-    (16,  4, 5,  7168, 48,  0.0, False),      # 16 staged tokens leave a short ring
+    (20,  1, 1,  16400, 32, 0.0, False),      # long rows
+    (16,  4, 5,  7168, 48,  0.0, False),
     (14,  3, 4,  64,   8208, 0.3, False),
     (9,   2, 3,  9216, 9232, 0.0, True),
     (16,  1, 1,  16400, 32, 0.0, False),
