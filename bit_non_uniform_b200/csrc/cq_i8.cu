@@ -351,19 +351,25 @@ struct I8MoePlan {
 //   * up to 32 routes, which one warp plans: 13.7 / 17.5 (4 experts 512 x 256,
 //     32 routes), 19.6 / 25.4 (16 of 1024 x 1024), 112 / 130 (16 of 7168 x
 //     2048); just above, 20.4 / 17.6 (16 of 512 x 256, 48 routes);
-//   * experts of 2 MB and more, up to 4 routes each: 54 / 55 (128 routes of 32
+//   * experts of 2 MB and more, up to 5 routes each: 54 / 55 (128 routes of 32
 //     experts 2048 x 1024), 231 / 238 (of 32 experts 7168 x 2048), 1665 / 1656
-//     (1024 of 256); at 8 each 255 / 242 (256 of 32).  Smaller experts leave no
-//     such range: 45 / 42 at 128 routes of 128 experts 1024 x 512;
+//     (1024 of 256); at 8 each 255 / 242 (256 of 32);
+//   * experts of 0.5 to 2 MB, up to 128 routes and 5 each: within 12%, 34.3 /
+//     31.2 at 96 and 44.6 / 42.4 at 128 routes (64 and 128 experts 1024 x 512),
+//     and ahead when some routes are dropped (22.9 / 24.8: 108 routes, three
+//     quarters dropped, 50 of 336 x 1040).  Above, 55 / 49 at 256.  Smaller ones
+//     leave no such range: 24.6 / 17.5 at 64 routes of 128 experts 256 x 128;
 //   * in several streamed launches: 2472 / 1720 at 144 tokens, top 8 of 256
 //     experts 7168 x 2048; 15976 / 5793 at 256 tokens, top 16 of 896.
-// Dropped routes count: the host does not know them.
+// Dropped routes count in all this: the host does not know them.
 // Tiles of 64 routes up to 96 each: 531 us against 562 with 128 at 48 routes
 // each (64 experts 7168 x 2048), 720 against 722 at 96, 1007 against 831 at
 // 128.  (256 routes, one CTA per SM: 1470 us at 256 each, 1293 with 128.)
 static bool i8_moe_sorted(int64_t routes, int64_t E, int64_t H, int64_t I, int k) {
+  const int64_t bytes = 3 * H * I;
   if (routes <= 32) return false;
-  return routes > kI8MaxRoutes / k * k || 3 * H * I < (2 << 20) || routes > 4 * E;
+  if (routes > kI8MaxRoutes / k * k || bytes < (1 << 19)) return true;
+  return routes > 5 * E || (bytes < (2 << 20) && routes > 128);
 }
 
 // Routes of one sorted launch: every further launch reads the experts again,

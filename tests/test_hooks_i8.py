@@ -98,9 +98,14 @@ def test_small_experts_are_streamed_for_few_routes_only(lib):
                     (1024, 64, 80)):
         assert moe_path(lib, 16, 2, E, H, I)[0] == STREAM, E
         assert moe_path(lib, 17, 2, E, H, I)[0] == SORTED, E
+    # middling ones up to 128 routes, 5 each
+    assert moe_path(lib, 16, 8, 128, 1024, 512)[0] == STREAM
+    assert moe_path(lib, 17, 8, 128, 1024, 512)[0] == SORTED
+    assert moe_path(lib, 20, 2, 8, 1024, 512)[0] == STREAM
+    assert moe_path(lib, 21, 2, 8, 1024, 512)[0] == SORTED
     # large ones while their weights bound both
-    assert moe_path(lib, 32, 4, 32, 2048, 1024)[0] == STREAM
-    assert moe_path(lib, 33, 4, 32, 2048, 1024)[0] == SORTED
+    assert moe_path(lib, 40, 4, 32, 2048, 1024)[0] == STREAM
+    assert moe_path(lib, 41, 4, 32, 2048, 1024)[0] == SORTED
 
 
 def test_a_sorted_launch_holds_more_routes_of_more_experts(lib):
